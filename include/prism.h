@@ -84,6 +84,12 @@ enum prism_chain {
   PRISM_CHAIN_GELU = 1    /* r_l = r_{l-1} - GELU(g_l * r_{l-1}), GELU(x) = x Phi(x) (erf form) */
 };
 
+/* Activation of the gated norm's gate: g sigmoid(g), or sigmoid(g). */
+enum prism_act {
+  PRISM_ACT_SILU = 0,
+  PRISM_ACT_SIGMOID = 1
+};
+
 enum prism_status {
   PRISM_OK = 0,
   PRISM_ERR_INVALID_ARG = 1, /* NULL where required, non-positive size, L < 1, W < 1, ... */
@@ -91,14 +97,16 @@ enum prism_status {
   PRISM_ERR_WORKSPACE = 3,   /* workspace smaller than prism_scan_fwd_workspace_size() */
   PRISM_ERR_CUDA = 4,        /* a CUDA runtime call or kernel launch failed */
   PRISM_ERR_TIMEOUT = 5,     /* a bounded device-side wait expired (from prism_stream_status) */
-  PRISM_ERR_BOUNDS = 6       /* debug build only: a kernel computed an index outside its buffer
-                                and skipped the access (from prism_stream_status) */
+  PRISM_ERR_BOUNDS = 6       /* an id outside the table of prism_embed_fwd / prism_embed_bwd, or,
+                                in the debug build, a kernel index outside its buffer; the kernel
+                                recorded it and skipped the access (from prism_stream_status) */
 };
 
 /* Limits of this build (checked; larger values return PRISM_ERR_UNSUPPORTED). */
 #define PRISM_MAX_HEAD_DIM 128 /* d_k, d_v in {16, 32, 64, 128} */
 #define PRISM_MAX_L 16         /* 1 <= L <= 16 */
 #define PRISM_MAX_W 8          /* 1 <= W <= 8 */
+#define PRISM_MAX_WIDTH 8192   /* row width D of the block norm and the embedding */
 
 /*
  * prism_scan_fwd - the whole mixer forward: ShortConv anchor, residual chain,
@@ -356,8 +364,142 @@ int prism_decode_step(const void* q, const void* k, const void* v,
                       int B, int H, int d_k, int d_v, int L, int W, int dtype, int chain,
                       void* o, prism_stream_t stream);
 
+/*
+ * The operators around the mixer.  A layer of a model normalises the residual stream before
+ * the mixer, gates and normalises the mixer's readout, and adds its output back to the
+ * stream; before the first layer stands the embedding, behind the backward pass the optimiser.
+ * They follow the conventions above: dense device buffers, 16-byte aligned, no allocation and
+ * no synchronisation, statistics and sums in fp32, each output rounded once.  Rows of padding
+ * (t >= lengths[b]) are not read; their outputs are written as zero and they add nothing to
+ * the gradients of weights.  Every result is the same bit for bit on every run.  Weights and
+ * their gradients are fp32; activations and their gradients have the dtype of the call.  A
+ * buffer that a call writes may overlap no other buffer of the call, except where an argument
+ * below says that it may be exactly another one (PRISM_ERR_INVALID_ARG otherwise).
+ */
+
+/*
+ * prism_gated_norm_fwd - the norm of the mixer's readout with its output gate, one row per
+ * (token, head):  y = o / sqrt(mean(o^2) + eps) * weight * act(gate),  mean over d.
+ *   o       [B,T,H,d] dtype     (prism_decode_step's o: T = 1)
+ *   gate    [B,T,H,d] dtype or NULL (no gate).  The H * d values of one token are dense; tokens
+ *           are gate_stride elements apart (H * d when dense; more for a slice of a wider
+ *           projection; a multiple of 16 bytes; ignored when gate is NULL)
+ *   weight  [d] fp32, shared by the heads
+ *   y       [B,T,H,d] dtype (output); may be o
+ * d in {16, 32, 64, 128}; eps > 0; act is a prism_act.  One launch.
+ */
+int prism_gated_norm_fwd(const void* o, const void* gate, const float* weight, const int32_t* lengths,
+                         int B, int T, int H, int d, long long gate_stride, float eps, int act, int dtype,
+                         void* y, prism_stream_t stream);
+
+/*
+ * prism_gated_norm_bwd - gradients of <y, dy>:  d_o, d_gate (dense; NULL iff gate is NULL)
+ * [B,T,H,d] dtype and d_weight [d] fp32.  d_o may be dy; it is what prism_scan_bwd takes as dO.
+ * The statistics are computed again from o.  workspace: at least
+ * prism_gated_norm_bwd_workspace_size() bytes.  Two launches.
+ */
+size_t prism_gated_norm_bwd_workspace_size(int B, int T, int H, int d);
+
+int prism_gated_norm_bwd(const void* o, const void* gate, const float* weight, const void* dy,
+                         const int32_t* lengths, int B, int T, int H, int d, long long gate_stride, float eps,
+                         int act, int dtype, void* d_o, void* d_gate, float* d_weight,
+                         void* workspace, size_t workspace_bytes, prism_stream_t stream);
+
+/*
+ * prism_block_norm_fwd - the border between two blocks of the residual stream: the block's
+ * output y joins the stream x, and the next block's input is normalised.
+ *   z = y, or y / sqrt(mean(y^2) + eps) * post_weight where post_weight is given
+ *   x_out = x + res_scale * scale * z;   h = x_out / sqrt(mean(x_out^2) + eps) * weight
+ * (means over D; h is computed from x_out before its rounding)
+ *   x, x_out  [B,T,D] x_dtype; x_out may be x.  y NULL: x_out is not written, h is the norm of x
+ *   y, h      [B,T,D] dtype
+ *   weight, post_weight (or NULL), scale (or NULL: 1)  [D] fp32
+ * 1 <= D <= PRISM_MAX_WIDTH (any width; multiples of 8 take 16-byte accesses).  x_dtype and
+ * dtype: both PRISM_BF16, both PRISM_FP32, or an fp32 stream with bf16 blocks.  One launch.
+ */
+int prism_block_norm_fwd(const void* x, const void* y, const float* post_weight, const float* scale,
+                         const float* weight, const int32_t* lengths, int B, int T, int D,
+                         float res_scale, float eps, int x_dtype, int dtype,
+                         void* x_out, void* h, prism_stream_t stream);
+
+/*
+ * prism_block_norm_bwd - gradients of <x_out, dx_out> + <h, dh>, from the stored x_out (x
+ * itself when y is NULL) and y.
+ *   dh [B,T,D] dtype; dx_out [B,T,D] x_dtype or NULL (zero)
+ *   dx [B,T,D] x_dtype, may be dx_out; dy [B,T,D] dtype (NULL iff y is NULL)
+ *   d_weight, and where their vectors are given d_post_weight and d_scale: [D] fp32
+ * workspace: at least prism_block_norm_bwd_workspace_size() bytes.  Two launches.
+ */
+size_t prism_block_norm_bwd_workspace_size(int B, int T, int D);
+
+int prism_block_norm_bwd(const void* x_out, const void* y, const float* post_weight, const float* scale,
+                         const float* weight, const void* dh, const void* dx_out, const int32_t* lengths,
+                         int B, int T, int D, float res_scale, float eps, int x_dtype, int dtype,
+                         void* dx, void* dy, float* d_weight, float* d_post_weight, float* d_scale,
+                         void* workspace, size_t workspace_bytes, prism_stream_t stream);
+
+/*
+ * prism_embed_fwd - out[b,t] = scale * table[ids[b,t]].
+ *   ids    [B,T] int32 or int64 (ids_bits 32 or 64)
+ *   table  [V,D] table_dtype;  out [B,T,D] dtype (table_dtype, or bf16 of an fp32 table)
+ * An id outside [0, V) at a valid step reads nothing: its row is zero, and PRISM_ERR_BOUNDS is
+ * recorded in the status word.  1 <= D <= PRISM_MAX_WIDTH, V <= 2^30, B T < 2^31.  One launch.
+ */
+int prism_embed_fwd(const void* ids, const void* table, const int32_t* lengths, int B, int T, int V, int D,
+                    float scale, int ids_bits, int table_dtype, int dtype, void* out, prism_stream_t stream);
+
+/*
+ * prism_embed_bwd - the table's gradient:  d_table[v] = scale * sum of d_out[b,t] over the
+ * tokens with ids[b,t] = v, summed in fp32 in the order of the tokens.
+ *   d_out [B,T,D] dtype;  d_table [V,D] fp32
+ *   accumulate 0: every row of d_table is written (zero where no token names it); otherwise
+ *   the sums are added to what d_table holds and only the rows that a token names are touched
+ * Ids outside [0, V) give no gradient and are recorded as in prism_embed_fwd.  workspace: at
+ * least prism_embed_bwd_workspace_size() bytes (16 bytes a token for the sorted ids, 8 to 64 KB
+ * of counts and 8 D bytes for each of about 2048 runs of tokens).  Four to six launches.
+ */
+size_t prism_embed_bwd_workspace_size(int B, int T, int V, int D);
+
+int prism_embed_bwd(const void* ids, const void* d_out, const int32_t* lengths, int B, int T, int V, int D,
+                    float scale, int ids_bits, int dtype, int accumulate, float* d_table,
+                    void* workspace, size_t workspace_bytes, prism_stream_t stream);
+
+/* One parameter tensor of prism_adamw_step: n elements at each of the device pointers. */
+typedef struct prism_adamw_tensor {
+  void* param;            /* p_dtype, updated in place */
+  const void* grad;       /* g_dtype */
+  void* exp_avg;          /* first moment: fp32, or e4m3 codes (one byte) */
+  void* exp_avg_sq;       /* second moment: fp32, or the e4m3 codes of its square root */
+  float* exp_avg_scale;   /* 8-bit states: [ceil(n / 256)], value = code * scale; NULL with 32 bits */
+  float* exp_avg_sq_scale;
+  void* copy;             /* bf16 copy of an fp32 parameter, written; or NULL */
+  long long n;            /* 0: the tensor is skipped */
+  double weight_decay;
+} prism_adamw_tensor;
+
+/*
+ * prism_adamw_step - one AdamW step over `count` tensors.  `tensors` is a HOST array, read
+ * during the call only (a captured graph holds its contents).
+ *   g = grad_scale * grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ *   step      counts from 1; step_dev, when given, is read on the device instead (below 1 counts as 1)
+ *   lr        likewise lr_dev; both let a captured graph be replayed along a schedule
+ *   grad_scale  device scalar (such as a clipping factor) or NULL (1)
+ *   state_bits  32: fp32 moments.  8: blocks of 256 consecutive elements of a tensor hold their
+ *             moments as e4m3 codes times one scale, the block's largest magnitude / 448 (at
+ *             least 2^-126); the second moment is held as its square root, and one that is not
+ *             zero is never held as zero.  The update takes the moments before that rounding.
+ *             Zeros are a valid first state.  An infinity or NaN in a gradient makes its block
+ *             NaN.
+ * All parameters share p_dtype and all gradients g_dtype.  The scalars and the scales are
+ * 4-byte aligned.  One launch for up to 440 tensors.
+ */
+int prism_adamw_step(const prism_adamw_tensor* tensors, int count, int step, const int32_t* step_dev, double lr,
+                     const float* lr_dev, double beta1, double beta2, double eps, const float* grad_scale,
+                     int p_dtype, int g_dtype, int state_bits, prism_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the device status word of the
- * current device: PRISM_OK, PRISM_ERR_TIMEOUT, PRISM_ERR_BOUNDS (debug build only), or
+ * current device: PRISM_OK, PRISM_ERR_TIMEOUT, PRISM_ERR_BOUNDS, or
  * PRISM_ERR_CUDA if the synchronisation itself failed. */
 int prism_stream_status(prism_stream_t stream);
 

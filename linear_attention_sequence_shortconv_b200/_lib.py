@@ -45,6 +45,16 @@ EXPORTS = (
     "prism_scan_bwd",
     "prism_scan_bwd_workspace_size",
     "prism_state_affine",
+    "prism_gated_norm_fwd",
+    "prism_gated_norm_bwd",
+    "prism_gated_norm_bwd_workspace_size",
+    "prism_block_norm_fwd",
+    "prism_block_norm_bwd",
+    "prism_block_norm_bwd_workspace_size",
+    "prism_embed_fwd",
+    "prism_embed_bwd",
+    "prism_embed_bwd_workspace_size",
+    "prism_adamw_step",
     "prism_scan_fwd_uses_tensor_cores",
     "prism_scan_fwd_launches",
     "prism_scan_fwd_split_chunks",
@@ -103,6 +113,28 @@ def lib() -> ctypes.CDLL:
     L.prism_scan_bwd.restype = ci
     L.prism_state_affine.argtypes = [fp, fp, fp, fp, ci, ci, ci, vp]
     L.prism_state_affine.restype = ci
+    cf, cd, cl = ctypes.c_float, ctypes.c_double, ctypes.c_longlong
+    L.prism_gated_norm_fwd.argtypes = [vp, vp, fp, i32p, ci, ci, ci, ci, cl, cf, ci, ci, vp, vp]
+    L.prism_gated_norm_fwd.restype = ci
+    L.prism_gated_norm_bwd_workspace_size.argtypes = [ci] * 4
+    L.prism_gated_norm_bwd_workspace_size.restype = cs
+    L.prism_gated_norm_bwd.argtypes = [vp, vp, fp, vp, i32p, ci, ci, ci, ci, cl, cf, ci, ci, vp, vp, fp, vp, cs, vp]
+    L.prism_gated_norm_bwd.restype = ci
+    L.prism_block_norm_fwd.argtypes = [vp, vp, fp, fp, fp, i32p, ci, ci, ci, cf, cf, ci, ci, vp, vp, vp]
+    L.prism_block_norm_fwd.restype = ci
+    L.prism_block_norm_bwd_workspace_size.argtypes = [ci] * 3
+    L.prism_block_norm_bwd_workspace_size.restype = cs
+    L.prism_block_norm_bwd.argtypes = ([vp, vp, fp, fp, fp, vp, vp, i32p, ci, ci, ci, cf, cf, ci, ci]
+                                       + [vp, vp, fp, fp, fp, vp, cs, vp])
+    L.prism_block_norm_bwd.restype = ci
+    L.prism_embed_fwd.argtypes = [vp, vp, i32p, ci, ci, ci, ci, cf, ci, ci, ci, vp, vp]
+    L.prism_embed_fwd.restype = ci
+    L.prism_embed_bwd_workspace_size.argtypes = [ci] * 4
+    L.prism_embed_bwd_workspace_size.restype = cs
+    L.prism_embed_bwd.argtypes = [vp, vp, i32p, ci, ci, ci, ci, cf, ci, ci, ci, fp, vp, cs, vp]
+    L.prism_embed_bwd.restype = ci
+    L.prism_adamw_step.argtypes = [vp, ci, ci, i32p, cd, fp, cd, cd, cd, fp, ci, ci, ci, vp]
+    L.prism_adamw_step.restype = ci
     L.prism_scan_fwd_uses_tensor_cores.argtypes = [ci] * 6
     L.prism_scan_fwd_uses_tensor_cores.restype = ci
     L.prism_scan_fwd_launches.argtypes = [ci] * 9

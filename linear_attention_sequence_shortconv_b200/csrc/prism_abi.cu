@@ -120,10 +120,10 @@ const char* prism_status_string(int code) {
     case PRISM_OK: return "PRISM_OK";
     case PRISM_ERR_INVALID_ARG: return "PRISM_ERR_INVALID_ARG: a required pointer is NULL or a size is out of range";
     case PRISM_ERR_UNSUPPORTED: return "PRISM_ERR_UNSUPPORTED: valid arguments this build does not implement (head size, width, chunk, alignment or device)";
-    case PRISM_ERR_WORKSPACE: return "PRISM_ERR_WORKSPACE: workspace smaller than prism_scan_fwd_workspace_size()";
+    case PRISM_ERR_WORKSPACE: return "PRISM_ERR_WORKSPACE: workspace smaller than the call's workspace_size query";
     case PRISM_ERR_CUDA: return "PRISM_ERR_CUDA: a CUDA runtime call or kernel launch failed";
     case PRISM_ERR_TIMEOUT: return "PRISM_ERR_TIMEOUT: a bounded device-side wait expired";
-    case PRISM_ERR_BOUNDS: return "PRISM_ERR_BOUNDS: a kernel computed an index outside its buffer (debug build)";
+    case PRISM_ERR_BOUNDS: return "PRISM_ERR_BOUNDS: an id outside the embedding table, or (debug build) a kernel index outside its buffer";
     default: return "PRISM: unknown status code";
   }
 }
