@@ -6,17 +6,19 @@
 // Tokens of padding (t >= lengths[b]) are not read: their output row is zero and they give no
 // gradient.  So is an id outside [0, V), which is recorded in the status word as well.
 //
-// Backward: the tokens are sorted by id (a stable radix sort of (id, token) pairs, two or
-// three passes of up to ten bits), so that a table row's summands stand next to each other in
-// the order of the tokens.  Then one launch sums the runs: the sorted positions are cut into
-// chunks of equal length, each thread group walks one chunk with its columns in registers and
-// writes every run that lies inside the chunk; a run that crosses a chunk's border leaves
-// partial sums, which a last launch adds from left to right.  No floating-point atomics, so
-// the result does not depend on any order of execution.  Rows without a token are written as
-// zero by further blocks of the summing launch, so a dense gradient is written exactly once.
+// Backward: the tokens are sorted by id (a stable radix sort of (id, token) pairs in passes of
+// up to ten bits), so that a table row's summands stand next to each other in the order of
+// the tokens.  Then one launch sums the runs: the sorted positions are cut into chunks of
+// equal length, each thread group walks one chunk with its columns in registers and writes
+// every run that lies inside the chunk; a run that crosses a chunk's border leaves partial
+// sums, which a last launch adds in a fixed order.  No floating-point atomics, so the result
+// does not depend on any order of execution.  Rows without a token are written as zero by
+// further blocks of the summing launch, so a dense gradient is written exactly once.
 //
 // Bound by memory: d_out is read once and the table's gradient is written once; the pairs are
 // 8 bytes a token and pass.
+#include <cooperative_groups.h>
+
 #include "embed.cuh"
 #include "rowops.cuh"
 
@@ -28,8 +30,8 @@ constexpr int kFwdThreads = 256;
 
 // One id; `key` of a token that takes no part is V.
 template <typename I>
-__device__ __forceinline__ uint32_t token_key(const EmbedParams& p, long long n, bool small) {
-  if (!token_valid(n, p.T, p.lengths, small)) return (uint32_t)p.V;
+__device__ __forceinline__ uint32_t token_key(const EmbedParams& p, long long n) {
+  if (!token_valid(n, p.T, p.lengths)) return (uint32_t)p.V;
   const long long id = static_cast<const I*>(p.ids)[n];
   if (id >= 0 && id < p.V) return (uint32_t)id;
   record_status(p.status, PRISM_ERR_BOUNDS);
@@ -43,7 +45,7 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(EmbedParams p, i
   __shared__ uint32_t key[kEmbedFwdTile];
   const long long first = (long long)blockIdx.x * tile;
   const int rows = (int)(p.N - first < tile ? p.N - first : tile);
-  for (int i = threadIdx.x; i < rows; i += kFwdThreads) key[i] = token_key<I>(p, first + i, true);
+  for (int i = threadIdx.x; i < rows; i += kFwdThreads) key[i] = token_key<I>(p, first + i);
   __syncthreads();
   const W* table = static_cast<const W*>(p.table);
   T* out = static_cast<T*>(p.out) + first * p.D;
@@ -66,65 +68,69 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(EmbedParams p, i
 }
 
 // ------------------------------------------------------------------------------------ the sort
-constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 1 << kEmbedMaxDigit;
-constexpr uint32_t kNoKey = 0xffffffffu;  // a place behind the tile's last token
+constexpr uint32_t kNoKey = 0xffffffffu;  // a place behind the last token
 
-// Counts of the first digit per tile; clears the later digits' counts of this tile.
-template <typename I>
-__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(EmbedParams p, EmbedPlan plan) {
-  __shared__ int count[kMaxBins];
-  const int bins = 1 << plan.digit;
-  for (int i = threadIdx.x; i < bins; i += kSortThreads) count[i] = 0;
-  __syncthreads();
-  const long long first = (long long)blockIdx.x * plan.tile;
-  const long long last = first + plan.tile < p.N ? first + plan.tile : p.N;
-  for (long long n = first + threadIdx.x; n < last; n += kSortThreads)
-    atomicAdd(&count[token_key<I>(p, n, true) & (bins - 1)], 1);
-  __syncthreads();
-  for (int i = threadIdx.x; i < bins; i += kSortThreads) {
-    p.hist[(size_t)blockIdx.x * bins + i] = count[i];
-    for (int q = 1; q < plan.passes; ++q) p.hist[((size_t)q * plan.tiles + blockIdx.x) * bins + i] = 0;
+// Programmatic launch of the next kernel of the chain: it may start once every block of this one
+// has said so, and waits for this one's end before it reads its results.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Stable ranks of a warp's 32 * KPT consecutive keys among the equal digits of the warp, and
+// the warp's counts per digit (`count`, zero before).  The lanes of equal digit are found by one
+// vote per bit.
+template <int KPT>
+__device__ __forceinline__ void rank_in_warp(const uint32_t (&key)[KPT], int shift, int bits, int lane,
+                                             unsigned short* count, int (&rank)[KPT]) {
+#pragma unroll
+  for (int i = 0; i < KPT; ++i) {
+    const bool in = key[i] != kNoKey;
+    const uint32_t digit = (key[i] >> shift) & ((1u << bits) - 1);
+    uint32_t same = __ballot_sync(0xffffffffu, in);
+    if (!in) same = ~same;
+#pragma unroll
+    for (int b = 0; b < kEmbedMaxDigit; ++b) {
+      if (b >= bits) break;  // the same for all lanes
+      const bool bit = (digit >> b) & 1;
+      const uint32_t set = __ballot_sync(0xffffffffu, bit);
+      same &= bit ? set : ~set;
+    }
+    const int leader = __ffs(same) - 1;
+    int start = 0;
+    if (in && lane == leader) {
+      start = count[digit];
+      count[digit] = (unsigned short)(start + __popc(same));
+    }
+    rank[i] = __shfl_sync(0xffffffffu, start, leader) + __popc(same & ((1u << lane) - 1));
+    __syncwarp();
   }
 }
 
-// One pass: a tile's pairs move to their places for digit `pass`.  Every block adds up the
-// counts of all tiles itself (they are few, and stay in L2).  Within a tile the warps take
-// consecutive runs of 32 * ROUNDS pairs; a pair's rank is the number of equal digits before
-// it, counted per warp, then over the warps.  The next digit's counts are gathered on the
-// way (integers, so their order does not matter).
-template <typename I, int ROUNDS>
-__global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(EmbedParams p, EmbedPlan plan, int pass) {
-  __shared__ unsigned short warp_count[kSortWarps][kMaxBins];
-  __shared__ int base[kMaxBins], step[kMaxBins];
-  __shared__ int warp_total[kSortWarps];
-  const int bins = 1 << plan.digit, shift = pass * plan.digit;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int* hist = p.hist + (size_t)pass * plan.tiles * bins;
-  int* next = pass + 1 < plan.passes ? p.hist + (size_t)(pass + 1) * plan.tiles * bins : nullptr;
-  const uint32_t* key_in = pass ? p.keys[(pass - 1) & 1] : nullptr;
-  const uint32_t* tok_in = pass ? p.toks[(pass - 1) & 1] : nullptr;
-  uint32_t* key_out = p.keys[pass & 1];
-  uint32_t* tok_out = p.toks[pass & 1];
-
-  // base[b] = pairs with a smaller digit + pairs of digit b in earlier tiles
-  int total[kMaxBins / kSortThreads], before[kMaxBins / kSortThreads], sum = 0;
+// The warps' counts of digit b become their exclusive prefix over the warps; returns the sum.
+template <int WARPS>
+__device__ __forceinline__ int prefix_over_warps(unsigned short* count, int stride, int b) {
+  int c[WARPS], s = 0;
 #pragma unroll
-  for (int j = 0; j < kMaxBins / kSortThreads; ++j) {
-    // consecutive bins per thread, so that one scan over the threads orders all bins
-    const int b = threadIdx.x * (kMaxBins / kSortThreads) + j;
-    total[j] = before[j] = 0;
-    if (b < bins) {
-#pragma unroll 8
-      for (int t = 0; t < plan.tiles; ++t) {
-        const int c = hist[(size_t)t * bins + b];
-        total[j] += c;
-        if (t < (int)blockIdx.x) before[j] += c;
-      }
-    }
-    sum += total[j];
+  for (int w = 0; w < WARPS; ++w) c[w] = count[w * stride + b];
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    count[w * stride + b] = (unsigned short)s;
+    s += c[w];
   }
-  int scan = sum;
+  return s;
+}
+
+// The cluster's barrier in its two halves; what a thread wrote before arriving is seen by the
+// whole cluster after the wait.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Exclusive scan of one value per thread over a block of `warps` warps (warp_total: shared).
+__device__ __forceinline__ int block_exclusive_scan(int x, int warps, int* warp_total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int scan = x;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, scan, off);
@@ -132,73 +138,231 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(EmbedParams p, 
   }
   if (lane == 31) warp_total[warp] = scan;
   __syncthreads();
-  int run = scan - sum;
-  for (int w = 0; w < warp; ++w) run += warp_total[w];
+  if (warp == 0) {
+    int t = lane < warps ? warp_total[lane] : 0;
 #pragma unroll
-  for (int j = 0; j < kMaxBins / kSortThreads; ++j) {
-    const int b = threadIdx.x * (kMaxBins / kSortThreads) + j;
-    if (b < bins) base[b] = run + before[j];
-    run += total[j];
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, t, off);
+      if (lane >= off) t += y;
+    }
+    if (lane < warps) warp_total[lane] = t;
   }
-
-  const long long first = (long long)blockIdx.x * plan.tile;
-  const long long last = first + plan.tile < p.N ? first + plan.tile : p.N;
-  for (int b = threadIdx.x; b < bins; b += kSortThreads) step[b] = 0;
   __syncthreads();
-  for (long long sub = first; sub < last; sub += kSortThreads * ROUNDS) {
-    for (int b = threadIdx.x; b < bins; b += kSortThreads) base[b] += step[b];
-    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) warp_count[i >> plan.digit][i & (bins - 1)] = 0;
-    __syncthreads();
-    uint32_t key[ROUNDS], tok[ROUNDS];
-    int rank[ROUNDS];
+  return scan - x + (warp ? warp_total[warp - 1] : 0);
+}
+
+// Up to 1024 * KPT * (cluster size) tokens: the whole sort in one launch of one cluster.  In a
+// pass a block ranks its pairs, exchanges its counts per digit with the other blocks through
+// distributed shared memory, orders the pairs by digit in its shared memory and writes them
+// out from there, so that the pairs of a digit leave in runs.  The cluster's barrier orders a
+// pass's pairs before the next one's reads.
+constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
+
+template <typename I, int KPT>
+__global__ void __launch_bounds__(kClusterThreads) sort_cluster_kernel(EmbedParams p, EmbedPlan plan) {
+  extern __shared__ __align__(16) char sort_smem[];
+  const int bins = 1 << plan.digit;
+  uint2* staged = reinterpret_cast<uint2*>(sort_smem);                      // [1024 KPT] pairs by digit
+  int* total = reinterpret_cast<int*>(staged + kClusterThreads * KPT);      // [bins] this block's counts
+  int* local = total + bins;                                                // [bins] first staged place
+  int* base = local + bins;                                                 // [bins] first place in the output
+  unsigned short* count = reinterpret_cast<unsigned short*>(base + bins);   // [warps][bins]
+  __shared__ int warp_total[2][kClusterWarps];
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int blocks = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const long long block0 = (long long)me * kClusterThreads * KPT, first = block0 + warp * 32 * KPT + lane;
+  const int mine = (int)(p.N - block0 < kClusterThreads * KPT ? (p.N > block0 ? p.N - block0 : 0) : kClusterThreads * KPT);
+  launch_dependents();
+  for (int pass = 0; pass < plan.passes; ++pass) {
+    const int shift = pass * plan.digit;
+    const uint2* in = pass & 1 ? p.pairs[0] : p.pairs[1];
+    uint32_t key[KPT], tok[KPT];
+    int rank[KPT];
 #pragma unroll
-    for (int i = 0; i < ROUNDS; ++i) {
-      const long long n = sub + (long long)warp * 32 * ROUNDS + 32 * i + lane;
+    for (int i = 0; i < KPT; ++i) {
+      const long long n = first + 32 * i;
       key[i] = kNoKey;
-      tok[i] = 0;
-      if (n < last) {
-        key[i] = pass ? key_in[n] : token_key<I>(p, n, true);
-        tok[i] = pass ? tok_in[n] : (uint32_t)n;
+      tok[i] = (uint32_t)n;
+      if (n < p.N) {
+        if (pass) {  // the pairs of an earlier pass come from other SMs: not through this one's L1
+          const uint2 x = __ldcg(in + n);
+          key[i] = x.x;
+          tok[i] = x.y;
+        } else {
+          key[i] = token_key<I>(p, n);
+        }
       }
     }
-#pragma unroll
-    for (int i = 0; i < ROUNDS; ++i) {
-      const bool in = key[i] != kNoKey;
-      const uint32_t digit = in ? (key[i] >> shift) & (bins - 1) : kNoKey;
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      const int leader = __ffs(same) - 1;
-      int start = 0;
-      if (in && lane == leader) {
-        start = warp_count[warp][digit];
-        warp_count[warp][digit] = (unsigned short)(start + __popc(same));
-      }
-      rank[i] = __shfl_sync(0xffffffffu, start, leader) + __popc(same & ((1u << lane) - 1));
-      __syncwarp();
-    }
+    uint32_t* zero = reinterpret_cast<uint32_t*>(count);
+    for (int i = threadIdx.x; i < kClusterWarps * bins / 2; i += kClusterThreads) zero[i] = 0;
     __syncthreads();
-    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
-      int s = 0;
-#pragma unroll
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int c = warp_count[w][b];
-        warp_count[w][b] = (unsigned short)s;
-        s += c;
-      }
-      step[b] = s;
-    }
+    rank_in_warp<KPT>(key, shift, plan.digit, lane, count + warp * bins, rank);
     __syncthreads();
+    const int b = threadIdx.x;  // bins <= threads
+    int here = 0;
+    if (b < bins) total[b] = here = prefix_over_warps<kClusterWarps>(count, bins, b);
+    cluster_arrive();
+    const int staged_at = block_exclusive_scan(here, kClusterWarps, warp_total[0]);
+    if (b < bins) local[b] = staged_at;
+    cluster_wait();
+    int all = 0, before = 0;
+    if (b < bins) {
 #pragma unroll
-    for (int i = 0; i < ROUNDS; ++i) {
+      for (int r = 0; r < kEmbedCluster; ++r) {
+        const int c = r < blocks ? cluster.map_shared_rank(total, r)[b] : 0;
+        all += c;
+        before += r < me ? c : 0;
+      }
+    }
+    const int start = block_exclusive_scan(all, kClusterWarps, warp_total[1]);  // its barriers publish local
+    if (b < bins) base[b] = start + before - staged_at;
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
       if (key[i] == kNoKey) continue;
       const uint32_t digit = (key[i] >> shift) & (bins - 1);
-      const int at = base[digit] + warp_count[warp][digit] + rank[i];
+      staged[local[digit] + count[warp * bins + digit] + rank[i]] = make_uint2(key[i], tok[i]);
+    }
+    __syncthreads();
+    uint2* out = pass & 1 ? p.pairs[1] : p.pairs[0];
+    for (int i = threadIdx.x; i < mine; i += kClusterThreads) {
+      const uint2 x = staged[i];
+      const int at = base[(x.x >> shift) & (bins - 1)] + i;
+      if (in_bounds(at, p.N, p.status)) out[at] = x;
+    }
+    cluster_arrive();  // the pairs are out, and nobody reads this block's counts any more
+    cluster_wait();
+  }
+}
+
+// More tokens: counts per tile, then for each pass a scan of all tiles' counts and the move of
+// the tiles' pairs.
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+
+// Counts of the first digit per tile; clears the later digits' counts of this tile.
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(EmbedParams p, EmbedPlan plan) {
+  __shared__ int count[kMaxBins];
+  const int bins = 1 << plan.digit;
+  launch_dependents();
+  for (int i = threadIdx.x; i < bins; i += kSortThreads) count[i] = 0;
+  __syncthreads();
+  const long long first = (long long)blockIdx.x * plan.tile;
+  const long long last = first + plan.tile < p.N ? first + plan.tile : p.N;
+  for (long long n = first + threadIdx.x; n < last; n += kSortThreads)
+    atomicAdd(&count[token_key<I>(p, n) & (bins - 1)], 1);
+  __syncthreads();
+  for (int i = threadIdx.x; i < bins; i += kSortThreads) {
+    p.hist[(size_t)blockIdx.x * bins + i] = count[i];
+    for (int q = 1; q < plan.passes; ++q) p.hist[((size_t)q * plan.tiles + blockIdx.x) * bins + i] = 0;
+  }
+}
+
+// hist[tile][bin] of one pass becomes the number of the bin's pairs in earlier tiles, totals[bin]
+// that in all tiles.  A block takes 32 bins (one per lane), a warp of it four of the tiles.
+constexpr int kScanThreads = 1024, kTilesPerWarp = 4;  // 128 tiles at most
+
+__global__ void __launch_bounds__(kScanThreads) sort_scan_kernel(EmbedParams p, EmbedPlan plan, int pass) {
+  __shared__ int sum[32][33];
+  const int bins = 1 << plan.digit, warp = threadIdx.x / 32, lane = threadIdx.x % 32, b = blockIdx.x * 32 + lane;
+  int* hist = p.hist + (size_t)pass * plan.tiles * bins;
+  int c[kTilesPerWarp], s = 0;
+  launch_dependents();
+  wait_for_previous();
+#pragma unroll
+  for (int i = 0; i < kTilesPerWarp; ++i) {
+    const int t = warp * kTilesPerWarp + i;
+    c[i] = t < plan.tiles && b < bins ? hist[(size_t)t * bins + b] : 0;
+    s += c[i];
+  }
+  sum[warp][lane] = s;
+  __syncthreads();
+  int at = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) {
+    const int x = sum[w][lane];
+    at += w < warp ? x : 0;
+    all += x;
+  }
+  if (b >= bins) return;
+#pragma unroll
+  for (int i = 0; i < kTilesPerWarp; ++i) {
+    const int t = warp * kTilesPerWarp + i;
+    if (t < plan.tiles) hist[(size_t)t * bins + b] = at;
+    at += c[i];
+  }
+  if (warp == 0) p.totals[pass * bins + b] = all;
+}
+
+// A tile's pairs move to their places for digit `pass`, in rounds of 512 * KPT; the next
+// digit's counts are gathered on the way (integers, so their order does not matter).
+template <typename I, int KPT>
+__global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(EmbedParams p, EmbedPlan plan, int pass) {
+  __shared__ unsigned short count[kSortWarps * kMaxBins];
+  __shared__ int base[kMaxBins], step[kMaxBins];
+  const int bins = 1 << plan.digit, shift = pass * plan.digit;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int* hist = p.hist + ((size_t)pass * plan.tiles + blockIdx.x) * bins;
+  int* next = pass + 1 < plan.passes ? p.hist + (size_t)(pass + 1) * plan.tiles * bins : nullptr;
+  const uint2* in = pass & 1 ? p.pairs[0] : p.pairs[1];
+  uint2* out = pass & 1 ? p.pairs[1] : p.pairs[0];
+  __shared__ int warp_total[kSortWarps];
+  launch_dependents();
+  wait_for_previous();
+  {  // a thread takes two consecutive bins
+    static_assert(kMaxBins == 2 * kSortThreads, "two bins per thread");
+    const int b = 2 * threadIdx.x;
+    const int t0 = b < bins ? p.totals[pass * bins + b] : 0, t1 = b + 1 < bins ? p.totals[pass * bins + b + 1] : 0;
+    const int start = block_exclusive_scan(t0 + t1, kSortWarps, warp_total);
+    if (b < bins) base[b] = start + hist[b];
+    if (b + 1 < bins) base[b + 1] = start + t0 + hist[b + 1];
+    for (int i = threadIdx.x; i < bins; i += kSortThreads) step[i] = 0;
+    __syncthreads();
+  }
+  const long long first = (long long)blockIdx.x * plan.tile;
+  const long long last = first + plan.tile < p.N ? first + plan.tile : p.N;
+  for (long long sub = first; sub < last; sub += kSortThreads * KPT) {
+    for (int b = threadIdx.x; b < bins; b += kSortThreads) base[b] += step[b];  // each bin by its own thread
+    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) count[i] = 0;
+    uint32_t key[KPT], tok[KPT];
+    int rank[KPT];
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      const long long n = sub + (long long)warp * 32 * KPT + 32 * i + lane;
+      key[i] = kNoKey;
+      tok[i] = (uint32_t)n;
+      if (n < last) {
+        if (pass) {
+          const uint2 x = in[n];
+          key[i] = x.x;
+          tok[i] = x.y;
+        } else {
+          key[i] = token_key<I>(p, n);
+        }
+      }
+    }
+    __syncthreads();
+    rank_in_warp<KPT>(key, shift, plan.digit, lane, count + warp * bins, rank);
+    __syncthreads();
+    for (int b = threadIdx.x; b < bins; b += kSortThreads) step[b] = prefix_over_warps<kSortWarps>(count, bins, b);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      if (key[i] == kNoKey) continue;
+      const uint32_t digit = (key[i] >> shift) & (bins - 1);
+      const int at = base[digit] + count[warp * bins + digit] + rank[i];
       if (!in_bounds(at, p.N, p.status)) continue;
-      key_out[at] = key[i];
-      tok_out[at] = tok[i];
+      out[at] = make_uint2(key[i], tok[i]);
       if (next) atomicAdd(next + (size_t)(at / plan.tile) * bins + ((key[i] >> (shift + plan.digit)) & (bins - 1)), 1);
     }
     __syncthreads();
   }
+}
+
+// the last pass's output (no index into the parameters, which would copy them to local memory)
+__device__ __forceinline__ const uint2* sorted_pairs(const EmbedParams& p, const EmbedPlan& plan) {
+  return plan.passes & 1 ? p.pairs[0] : p.pairs[1];
 }
 
 // ------------------------------------------------------------------------------------ the sums
@@ -206,7 +370,25 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(EmbedParams p, 
 // tpr.  blockIdx.y is the tile of 8 tpr columns.
 constexpr int kSumThreads = 256;
 constexpr int kZeroRows = 64;  // table rows that one zeroing block looks after
-constexpr int kAhead = 4;      // rows in flight per thread
+constexpr int kLongChunks = 32;
+constexpr int kShortRun = 8;   // partial sums behind a run's first up to which one thread group joins it
+
+// Eight columns as they lie in memory.
+template <typename T>
+struct Raw {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void add_to(float (&x)[8]) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] += sizeof(T) == 4 ? __uint_as_float(w[i * sizeof(T) / 4])
+                             : __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
 
 template <bool VEC>
 struct Columns {
@@ -245,26 +427,33 @@ struct Columns {
   }
 };
 
-// first position in [0, N) whose key is at least v
-__device__ __forceinline__ int lower_bound(const uint32_t* keys, int N, uint32_t v) {
-  int lo = 0, hi = N;
+// First position in [0, N) whose key is at least v, found by a warp: 32 probes a step.
+__device__ __forceinline__ int lower_bound(const uint2* pairs, int N, uint32_t v, int lane) {
+  int lo = 0, hi = N;  // the answer is in [lo, hi]
   while (lo < hi) {
-    const int mid = lo + (hi - lo) / 2;
-    if (keys[mid] < v) lo = mid + 1;
-    else hi = mid;
+    const int step = (hi - lo + 32) / 33;  // at least 1
+    const long long at = (long long)lo + (long long)(lane + 1) * step - 1;
+    const bool less = at < hi && pairs[at].x < v;
+    const int n = __popc(__ballot_sync(0xffffffffu, less));  // the keys are sorted: a prefix of the probes
+    const long long top = (long long)lo + (long long)(n + 1) * step - 1;
+    lo += n * step;
+    if (top < hi) hi = (int)top;
   }
   return lo;
 }
 
 // table rows [v0, v0 + kZeroRows): those without a token become zero
-__device__ __forceinline__ void zero_absent_rows(const EmbedParams& p, const uint32_t* keys, long long v0) {
+__device__ __forceinline__ void zero_absent_rows(const EmbedParams& p, const uint2* pairs, long long v0) {
   __shared__ int range[2];
   __shared__ int present[kZeroRows];
   const int rows = (int)(p.V - v0 < kZeroRows ? p.V - v0 : kZeroRows);
-  if (threadIdx.x < 2) range[threadIdx.x] = lower_bound(keys, (int)p.N, (uint32_t)(v0 + (threadIdx.x ? rows : 0)));
-  if (threadIdx.x < kZeroRows) present[threadIdx.x] = 0;
+  if (threadIdx.x < 64) {  // two warps, one for each end
+    const int at = lower_bound(pairs, (int)p.N, (uint32_t)(v0 + (threadIdx.x < 32 ? 0 : rows)), threadIdx.x % 32);
+    if (threadIdx.x % 32 == 0) range[threadIdx.x / 32] = at;
+  }
+  for (int r = threadIdx.x; r < kZeroRows; r += blockDim.x) present[r] = 0;
   __syncthreads();
-  for (int i = range[0] + threadIdx.x; i < range[1]; i += blockDim.x) present[keys[i] - (uint32_t)v0] = 1;
+  for (int i = range[0] + threadIdx.x; i < range[1]; i += blockDim.x) present[pairs[i].x - (uint32_t)v0] = 1;
   __syncthreads();
   const float zero[8] = {};
   const bool vec = p.D % 8 == 0;
@@ -279,78 +468,165 @@ __device__ __forceinline__ void zero_absent_rows(const EmbedParams& p, const uin
   }
 }
 
+// Blocks below `zero_blocks` look after the rows without a token; a thread group of the others
+// walks the runs of one chunk, eight columns per thread (blockIdx.y: tile of 8 tpr columns).
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(EmbedParams p, EmbedPlan plan, int tpr, int groups,
-                                                                int sum_blocks) {
-  const uint32_t* keys = p.keys[(plan.passes - 1) & 1];
-  const uint32_t* toks = p.toks[(plan.passes - 1) & 1];
-  if ((int)blockIdx.x >= sum_blocks) {
-    if (blockIdx.y == 0) zero_absent_rows(p, keys, (long long)(blockIdx.x - sum_blocks) * kZeroRows);
+__global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(EmbedParams p, EmbedPlan plan, int tpr, int groups,
+                                                                   int zero_blocks) {
+  extern __shared__ uint2 staged_pairs[];  // of the block's positions
+  const uint2* pairs = sorted_pairs(p, plan);
+  launch_dependents();
+  wait_for_previous();
+  if ((int)blockIdx.x < zero_blocks) {
+    if (blockIdx.y == 0) zero_absent_rows(p, pairs, (long long)blockIdx.x * kZeroRows);
     return;
   }
+  const long long block = blockIdx.x - zero_blocks;
+  const int span = groups * plan.chunk;
+  const long long at0 = block * span;
+  const uint32_t none = (uint32_t)p.V;  // padding, and what lies behind the last token: sorts behind every id
+  for (int i = threadIdx.x; i < span; i += blockDim.x)
+    staged_pairs[i] = at0 + i < p.N ? pairs[at0 + i] : make_uint2(none, 0);
   const int group = threadIdx.x / tpr;
-  const long long c = (long long)blockIdx.x * groups + group;
-  if (c >= plan.chunks) return;
-  const int s = (int)c * plan.chunk, e = (int)(s + (long long)plan.chunk < p.N ? s + plan.chunk : p.N);
+  const long long c = block * groups + group, s0 = c * plan.chunk, e0 = s0 + plan.chunk;
+  const uint32_t prior = s0 > 0 && s0 < p.N ? pairs[s0 - 1].x : none, after = e0 < p.N ? pairs[e0].x : none;
+  __syncthreads();
+  if (group >= groups) return;
+  const uint2* pair = staged_pairs + group * plan.chunk;
+  uint32_t cur = pair[0].x;
+  if (cur == none) return;
   const Columns<VEC> col(threadIdx.x - group * tpr, tpr, blockIdx.y, p.D);
-  const uint32_t none = (uint32_t)p.V;
-  uint32_t cur = keys[s];
-  if (cur == none) return;  // padding sorts behind every id
   const T* d_out = static_cast<const T*>(p.d_out);
   float* head = p.part + (size_t)c * 2 * p.D;
-  bool from_before = s > 0 && keys[s - 1] == cur;
+  bool from_before = prior == cur;
   float acc[8];
   zero8(acc);
-  for (int i = s; i < e; i += kAhead) {
-    uint32_t key[kAhead];
-    float x[kAhead][8];
+  constexpr int kAhead = VEC ? 16 / sizeof(T) : 2;  // rows in flight per thread: 128 bytes of them
+  for (int i = 0; i < plan.chunk; i += kAhead) {    // plan.chunk is a multiple of kAhead
+    Raw<T> raw[VEC ? kAhead : 1];
+    float x[VEC ? 1 : kAhead][8];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      key[j] = i + j < e ? keys[i + j] : none;
-      if (key[j] != none) col.load(d_out + (size_t)toks[i + j] * p.D, x[j]);
+      const uint2 k = pair[i + j];
+      const T* row = d_out + (size_t)k.y * p.D;
+      if (VEC) {
+        if (k.x != none && col.first < p.D) raw[VEC ? j : 0].load(row + col.first);
+      } else if (k.x != none) {
+        col.load(row, x[VEC ? 0 : j]);
+      }
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (i + j >= e) break;
-      if (key[j] != cur) {
+      const uint32_t k = pair[i + j].x;
+      if (k != cur) {
         if (from_before) col.store(head, acc);
         else col.finish(p, cur, acc);
         from_before = false;
-        cur = key[j];
+        cur = k;
         if (cur == none) return;
         zero8(acc);
       }
+      if (VEC) {
+        raw[VEC ? j : 0].add_to(acc);
+      } else {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) acc[q] += x[j][q];
+        for (int q = 0; q < 8; ++q) acc[q] += x[VEC ? 0 : j][q];
+      }
     }
   }
-  const bool goes_on = e < p.N && keys[e] == cur;
   if (from_before) col.store(head, acc);
-  else if (goes_on) col.store(head + p.D, acc);  // this chunk's tail
+  else if (after == cur) col.store(head + p.D, acc);  // this chunk's tail
   else col.finish(p, cur, acc);
 }
 
-// The runs that cross a chunk's border: the group of the chunk where a run begins adds the
-// chunk's tail and the heads of the chunks it reaches, from left to right.
-template <bool VEC>
-__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(EmbedParams p, EmbedPlan plan, int tpr, int groups) {
-  const uint32_t* keys = p.keys[(plan.passes - 1) & 1];
-  const int group = threadIdx.x / tpr;
-  const long long c = (long long)blockIdx.x * groups + group;
-  if (c + 1 >= plan.chunks) return;
-  const int s = (int)c * plan.chunk, e = s + plan.chunk;  // not the last chunk: e < N
-  const uint32_t cur = keys[e - 1];
-  if (cur == (uint32_t)p.V || keys[e] != cur) return;
-  if (s > 0 && keys[s - 1] == cur) return;  // began earlier (the keys are sorted)
-  const Columns<VEC> col(threadIdx.x - group * tpr, tpr, blockIdx.y, p.D);
-  float acc[8], x[8];
-  col.load(p.part + ((size_t)c * 2 + 1) * p.D, acc);
-  for (long long n = c + 1; n < plan.chunks && keys[n * plan.chunk] == cur; ++n) {
-    col.load(p.part + (size_t)n * 2 * p.D, x);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) acc[q] += x[q];
+// The runs that cross a chunk's border: the chunk where a run begins holds its first partial
+// sum (its tail), the chunks it reaches hold the others (their heads).
+struct Runs {
+  const uint2* pairs;
+  uint32_t none;
+  int chunk, chunks;
+  // key at the first position of chunk n (`none` behind the last)
+  __device__ __forceinline__ uint32_t at(long long n) const { return n < chunks ? pairs[n * chunk].x : none; }
+  // the id of the run that begins in chunk c and goes on behind it, or `none`
+  __device__ __forceinline__ uint32_t begins(long long c) const {
+    if (c + 1 >= chunks) return none;
+    const uint32_t next = at(c + 1), last = pairs[(c + 1) * chunk - 1].x, prior = c ? pairs[c * chunk - 1].x : none;
+    return next == last && prior != last ? last : none;
   }
-  col.finish(p, cur, acc);
+};
+
+// A group of `width` threads (up to a warp's) holds 8 width columns; blockIdx.y is their tile.
+// Blocks below `short_blocks`: one group per chunk adds a run of up to kShortRun further partial
+// sums from left to right.  Further blocks look after kLongChunks chunks each and take the
+// longer runs that begin there: the block's groups add equal slices of the partial sums, whose
+// sums are then added from left to right.
+template <bool VEC>
+__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(EmbedParams p, EmbedPlan plan, int width,
+                                                                 int short_blocks) {
+  __shared__ uint32_t found;
+  __shared__ __align__(16) float slice[kSumThreads * 8];  // written in 16-byte pieces
+  const Runs runs{sorted_pairs(p, plan), (uint32_t)p.V, plan.chunk, plan.chunks};
+  const int groups = kSumThreads / width, group = threadIdx.x / width, gt = threadIdx.x - group * width;
+  const Columns<VEC> col(gt, width, blockIdx.y, p.D);
+  float acc[8], x[8];
+  wait_for_previous();
+  if ((int)blockIdx.x < short_blocks) {
+    if (group >= groups) return;
+    const long long c = (long long)blockIdx.x * groups + group;
+    const uint32_t id = runs.begins(c);
+    if (id == runs.none) return;
+    int heads = 0;
+#pragma unroll
+    for (int n = 1; n <= kShortRun + 1; ++n) heads += runs.at(c + n) == id;
+    if (heads > kShortRun) return;
+    col.load(p.part + ((size_t)c * 2 + 1) * p.D, acc);
+#pragma unroll 4
+    for (int n = 1; n <= heads; ++n) {
+      col.load(p.part + (size_t)(c + n) * 2 * p.D, x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[q] += x[q];
+    }
+    col.finish(p, id, acc);
+    return;
+  }
+  const long long c0 = (long long)(blockIdx.x - short_blocks) * kLongChunks;
+  if (threadIdx.x < kLongChunks) {
+    const uint32_t own = runs.begins(c0 + threadIdx.x);
+    const uint32_t far = __ballot_sync(0xffffffffu, own != runs.none && runs.at(c0 + threadIdx.x + kShortRun + 1) == own);
+    if (threadIdx.x == 0) found = far;
+  }
+  __syncthreads();
+  for (uint32_t left = found; left; left &= left - 1) {
+    const long long c = c0 + __ffs(left) - 1;
+    const uint32_t id = runs.at(c + 1);
+    long long heads = 0;  // chunks behind c that the run reaches: a prefix, since the keys are sorted
+    for (;;) {
+      const int got = __syncthreads_count(runs.at(c + 1 + heads + threadIdx.x) == id);
+      heads += got;
+      if (got < kSumThreads) break;
+    }
+    zero8(acc);
+    if (group < groups) {
+      const long long lo = heads * group / groups, hi = heads * (group + 1) / groups;
+      if (group == 0) col.load(p.part + ((size_t)c * 2 + 1) * p.D, acc);
+#pragma unroll 8
+      for (long long n = lo; n < hi; ++n) {
+        col.load(p.part + (size_t)(c + 1 + n) * 2 * p.D, x);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[q] += x[q];
+      }
+    }
+    store8(slice + 8 * threadIdx.x, acc);
+    __syncthreads();
+    if (group == 0) {
+      for (int g = 1; g < groups; ++g) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[q] += slice[8 * (g * width + gt) + q];
+      }
+      col.finish(p, id, acc);
+    }
+    __syncthreads();
+  }
 }
 
 template <typename I, typename W, typename T>
@@ -375,30 +651,82 @@ cudaError_t embed_fwd_ids(const EmbedParams& p, int table_dtype, int dtype, cuda
   return embed_fwd_types<I, float, float>(p, stream);
 }
 
+template <typename I, int KPT>
+cudaError_t sort_cluster(const EmbedParams& p, const EmbedPlan& plan, cudaStream_t stream) {
+  auto bytes = [](int digit) { return (size_t)kClusterThreads * KPT * 8 + (((size_t)kClusterWarps * 2 + 12) << digit); };
+  cudaError_t err = cudaFuncSetAttribute(sort_cluster_kernel<I, KPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)bytes(kEmbedMaxDigit));
+  if (err == cudaSuccess && plan.cluster > 8)
+    err = cudaFuncSetAttribute(sort_cluster_kernel<I, KPT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(plan.cluster);
+  cfg.blockDim = dim3(kClusterThreads);
+  cfg.dynamicSmemBytes = bytes(plan.digit);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = plan.cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sort_cluster_kernel<I, KPT>, p, plan);
+}
+
+// A launch that may overlap the end of the one before it (whose results its kernel waits for).
+template <typename... Args>
+cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                           Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename I, int KPT>
+cudaError_t sort_tiles(const EmbedParams& p, const EmbedPlan& plan, cudaStream_t stream) {
+  sort_count_kernel<I><<<plan.tiles, kSortThreads, 0, stream>>>(p, plan);
+  cudaError_t err = cudaGetLastError();
+  const int scans = ((1 << plan.digit) + 31) / 32;
+  for (int pass = 0; pass < plan.passes && err == cudaSuccess; ++pass) {
+    err = launch_chained(sort_scan_kernel, dim3(scans), kScanThreads, 0, stream, p, plan, pass);
+    if (err == cudaSuccess)
+      err = launch_chained(sort_pass_kernel<I, KPT>, dim3(plan.tiles), kSortThreads, 0, stream, p, plan, pass);
+  }
+  return err;
+}
+
 template <typename I>
 cudaError_t embed_sort(const EmbedParams& p, const EmbedPlan& plan, cudaStream_t stream) {
-  sort_count_kernel<I><<<plan.tiles, kSortThreads, 0, stream>>>(p, plan);
-  for (int pass = 0; pass < plan.passes; ++pass) {
-    if (plan.rounds == 2)
-      sort_pass_kernel<I, 2><<<plan.tiles, kSortThreads, 0, stream>>>(p, plan, pass);
-    else
-      sort_pass_kernel<I, 8><<<plan.tiles, kSortThreads, 0, stream>>>(p, plan, pass);
-  }
-  return cudaGetLastError();
+  if (plan.cluster) return plan.kpt == 1 ? sort_cluster<I, 1>(p, plan, stream) : sort_cluster<I, 2>(p, plan, stream);
+  return plan.kpt == 2 ? sort_tiles<I, 2>(p, plan, stream)
+         : plan.kpt == 4 ? sort_tiles<I, 4>(p, plan, stream) : sort_tiles<I, 8>(p, plan, stream);
 }
 
 template <typename T, bool VEC>
 cudaError_t embed_sums(const EmbedParams& p, const EmbedPlan& plan, cudaStream_t stream) {
   const int need = (p.D + 7) / 8;  // threads that hold a row
-  int tpr = need < kSumThreads ? need : kSumThreads;
-  const int groups = kSumThreads / tpr, tiles = (need + tpr - 1) / tpr;
+  const int tpr = need < kSumThreads ? need : kSumThreads;
+  // a block's pairs stay within 32 KB of shared memory
+  const int most = 4096 / plan.chunk, fit = kSumThreads / tpr, groups = fit < most ? fit : most;
+  const int tiles = (need + tpr - 1) / tpr, threads = tpr * groups < 64 ? 64 : tpr * groups;
   const int sum_blocks = (plan.chunks + groups - 1) / groups;
   const int zero_blocks = p.accumulate ? 0 : (int)(((long long)p.V + kZeroRows - 1) / kZeroRows);
-  embed_sum_kernel<T, VEC><<<dim3(sum_blocks + zero_blocks, tiles), tpr * groups, 0, stream>>>(p, plan, tpr, groups,
-                                                                                              sum_blocks);
-  if (plan.chunks > 1)
-    embed_join_kernel<VEC><<<dim3(sum_blocks, tiles), tpr * groups, 0, stream>>>(p, plan, tpr, groups);
-  return cudaGetLastError();
+  cudaError_t err = launch_chained(embed_sum_kernel<T, VEC>, dim3(sum_blocks + zero_blocks, tiles), threads,
+                                   (size_t)groups * plan.chunk * 8, stream, p, plan, tpr, groups, zero_blocks);
+  if (err != cudaSuccess || plan.chunks == 1) return err;
+  const int width = need < 32 ? need : 32, joins = kSumThreads / width;
+  const int short_blocks = (plan.chunks + joins - 1) / joins;
+  const int long_blocks = plan.chunks > kShortRun + 1 ? (plan.chunks + kLongChunks - 1) / kLongChunks : 0;
+  return launch_chained(embed_join_kernel<VEC>, dim3(short_blocks + long_blocks, (need + width - 1) / width),
+                        kSumThreads, 0, stream, p, plan, width, short_blocks);
 }
 
 }  // namespace

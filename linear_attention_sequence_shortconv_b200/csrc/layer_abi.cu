@@ -118,7 +118,7 @@ int prism_gated_norm_fwd(const void* o, const void* gate, const float* weight, c
   rc = prism::device_setup(&status);
   if (rc != PRISM_OK) return rc;
   const prism::GatedNormParams p{o, gate, weight, nullptr, lengths, y, nullptr, nullptr, (long long)toks * H,
-                                 gate_stride, T, H, eps};
+                                 gate_stride, prism::FastDiv(T), prism::FastDiv(H), eps};
   return launched(prism::launch_gated_norm_fwd(p, d, gate_kind(gate, act), dtype, cuda_stream(stream)));
 }
 
@@ -147,7 +147,7 @@ int prism_gated_norm_bwd(const void* o, const void* gate, const float* weight, c
   rc = prism::device_setup(&status);
   if (rc != PRISM_OK) return rc;
   const prism::GatedNormParams p{o, gate, weight, dy, lengths, d_o, d_gate, static_cast<float*>(workspace),
-                                 (long long)toks * H, gate_stride, T, H, eps};
+                                 (long long)toks * H, gate_stride, prism::FastDiv(T), prism::FastDiv(H), eps};
   return launched(prism::launch_gated_norm_bwd(p, d, gate_kind(gate, act), dtype, d_weight, cuda_stream(stream)));
 }
 
@@ -167,7 +167,7 @@ int prism_block_norm_fwd(const void* x, const void* y, const float* post_weight,
   rc = prism::device_setup(&status);
   if (rc != PRISM_OK) return rc;
   const prism::BlockNormParams p{x, y, post_weight, scale, weight, nullptr, nullptr, lengths, x_out, h, nullptr,
-                                 (long long)B * T, T, D, 0, 0, res_scale, eps};
+                                 (long long)B * T, prism::FastDiv(T), D, 0, 0, res_scale, eps};
   float* const sums[3] = {nullptr, nullptr, nullptr};
   return launched(prism::launch_block_norm(p, false, x_dtype, dtype, sums, cuda_stream(stream)));
 }
@@ -200,7 +200,7 @@ int prism_block_norm_bwd(const void* x_out, const void* y, const float* post_wei
   rc = prism::device_setup(&status);
   if (rc != PRISM_OK) return rc;
   const prism::BlockNormParams p{x_out, y, post_weight, scale, weight, dh, dx_out, lengths, dx, dy,
-                                 static_cast<float*>(workspace), (long long)B * T, T, D, 0, 0, res_scale, eps};
+                                 static_cast<float*>(workspace), (long long)B * T, prism::FastDiv(T), D, 0, 0, res_scale, eps};
   float* const sums[3] = {d_weight, d_post_weight, d_scale};
   return launched(prism::launch_block_norm(p, true, x_dtype, dtype, sums, cuda_stream(stream)));
 }
@@ -224,7 +224,7 @@ int prism_embed_fwd(const void* ids, const void* table, const int32_t* lengths, 
   p.lengths = lengths;
   p.out = out;
   p.N = (long long)n;
-  p.T = T;
+  p.T = prism::FastDiv(T);
   p.V = V;
   p.D = D;
   p.scale = scale;
@@ -257,14 +257,12 @@ int prism_embed_bwd(const void* ids, const void* d_out, const int32_t* lengths, 
   p.d_out = d_out;
   p.lengths = lengths;
   p.d_table = d_table;
-  for (int i = 0; i < 2; ++i) {
-    p.keys[i] = reinterpret_cast<uint32_t*>(ws + plan.off_pairs[2 * i]);
-    p.toks[i] = reinterpret_cast<uint32_t*>(ws + plan.off_pairs[2 * i + 1]);
-  }
+  for (int i = 0; i < 2; ++i) p.pairs[i] = reinterpret_cast<uint2*>(ws + plan.off_pairs[i]);
   p.hist = reinterpret_cast<int*>(ws + plan.off_hist);
+  p.totals = reinterpret_cast<int*>(ws + plan.off_totals);
   p.part = reinterpret_cast<float*>(ws + plan.off_part);
   p.N = (long long)n;
-  p.T = T;
+  p.T = prism::FastDiv(T);
   p.V = V;
   p.D = D;
   p.accumulate = accumulate != 0;

@@ -56,7 +56,6 @@ template <typename T, int LPR, int GATE>
 __global__ void __launch_bounds__(kGnThreads) gated_norm_fwd_kernel(GatedNormParams p) {
   constexpr int d = 8 * LPR, kPer = kGnThreads / LPR;
   const int lane = threadIdx.x % LPR;
-  const bool small = p.rows <= 0xffffffffll;
   float w[8], o[kGnRows][8], g[kGnRows][8];
   load8(p.weight + 8 * lane, w);
   long long row[kGnRows];
@@ -70,12 +69,12 @@ __global__ void __launch_bounds__(kGnThreads) gated_norm_fwd_kernel(GatedNormPar
     zero8(g[u]);
     if (!in[u]) continue;
     long long tok = 0;
-    if (GATE != kGateNone || p.lengths) tok = div_row(row[u], p.H, small);
-    valid[u] = token_valid(tok, p.T, p.lengths, small);
+    if (GATE != kGateNone || p.lengths) tok = p.H.div(row[u]);
+    valid[u] = token_valid(tok, p.T, p.lengths);
     if (!valid[u]) continue;
     load8(static_cast<const T*>(p.o) + row[u] * d + 8 * lane, o[u]);
     if (GATE != kGateNone)
-      load8(static_cast<const T*>(p.gate) + tok * p.gate_stride + (row[u] - tok * p.H) * d + 8 * lane, g[u]);
+      load8(static_cast<const T*>(p.gate) + tok * p.gate_stride + (row[u] - tok * p.H.d) * d + 8 * lane, g[u]);
   }
 #pragma unroll
   for (int u = 0; u < kGnRows; ++u) {
@@ -104,7 +103,6 @@ template <typename T, int LPR, int GATE>
 __global__ void __launch_bounds__(kGnThreads) gated_norm_bwd_kernel(GatedNormParams p) {
   constexpr int d = 8 * LPR, kPer = kGnThreads / LPR;
   const int lane = threadIdx.x % LPR;
-  const bool small = p.rows <= 0xffffffffll;
   float w[8], dw[8];
   load8(p.weight + 8 * lane, w);
   zero8(dw);
@@ -118,13 +116,13 @@ __global__ void __launch_bounds__(kGnThreads) gated_norm_bwd_kernel(GatedNormPar
     zero8(dy);
     if (in) {
       long long tok = 0;
-      if (GATE != kGateNone || p.lengths) tok = div_row(row, p.H, small);
-      valid = token_valid(tok, p.T, p.lengths, small);
+      if (GATE != kGateNone || p.lengths) tok = p.H.div(row);
+      valid = token_valid(tok, p.T, p.lengths);
       if (valid) {
         load8(static_cast<const T*>(p.o) + row * d + 8 * lane, o);
         load8(static_cast<const T*>(p.dy) + row * d + 8 * lane, dy);
         if (GATE != kGateNone)
-          load8(static_cast<const T*>(p.gate) + tok * p.gate_stride + (row - tok * p.H) * d + 8 * lane, g);
+          load8(static_cast<const T*>(p.gate) + tok * p.gate_stride + (row - tok * p.H.d) * d + 8 * lane, g);
       }
     }
     float s = 0.f, c = 0.f, dg[8], t[8];
@@ -154,7 +152,7 @@ __global__ void __launch_bounds__(kGnThreads) gated_norm_bwd_kernel(GatedNormPar
     store8(static_cast<T*>(p.y) + row * d + 8 * lane, d_o);
     if (GATE != kGateNone) store8(static_cast<T*>(p.d_gate) + row * d + 8 * lane, dg);
   }
-  __shared__ float sum[kPer][d];
+  __shared__ __align__(16) float sum[kPer][d];
   store8(&sum[threadIdx.x / LPR][8 * lane], dw);
   __syncthreads();
   for (int c = threadIdx.x; c < d; c += kGnThreads) {
@@ -255,7 +253,6 @@ __global__ void __launch_bounds__(kBnThreads) block_norm_fwd_kernel(BlockNormPar
   __shared__ float buf[kBnGroups][2][32][R];
   const int tpr = p.tpr, gt = threadIdx.x % tpr, group = threadIdx.x / tpr, D = p.D;
   GroupSum<R> sum{buf};
-  const bool small = p.rows <= 0xffffffffll;
   float w[E], k[E], wp[E];
   load_vec<E, VEC>(p.weight, gt, tpr, D, 1.f, w);
   if (DELTA) {
@@ -273,7 +270,7 @@ __global__ void __launch_bounds__(kBnThreads) block_norm_fwd_kernel(BlockNormPar
     for (int u = 0; u < R; ++u) {
       row[u] = base + (long long)group * R + u;
       in[u] = row[u] < p.rows;
-      ok[u] = in[u] && token_valid(row[u], p.T, p.lengths, small);
+      ok[u] = in[u] && token_valid(row[u], p.T, p.lengths);
       load_row<E, VEC>(static_cast<const X*>(p.x) + row[u] * D, gt, tpr, D, ok[u], x[u]);
       if (DELTA) load_row<E, VEC>(static_cast<const A*>(p.y) + row[u] * D, gt, tpr, D, ok[u], y[u]);
     }
@@ -324,7 +321,6 @@ __global__ void __launch_bounds__(kBnThreads) block_norm_bwd_kernel(BlockNormPar
   const int tpr = p.tpr, gt = threadIdx.x % tpr, group = threadIdx.x / tpr, D = p.D;
   GroupSum<N> sum{buf};
   GroupSum<1> sum1{buf1};
-  const bool small = p.rows <= 0xffffffffll;
   float w[E], k[E], wp[E], aw[E], ap[E], as[E];
   load_vec<E, VEC>(p.weight, gt, tpr, D, 1.f, w);
   if (DELTA) {
@@ -337,7 +333,7 @@ __global__ void __launch_bounds__(kBnThreads) block_norm_bwd_kernel(BlockNormPar
   for (int e = 0; e < E; ++e) aw[e] = ap[e] = as[e] = 0.f;
   for (long long base = (long long)blockIdx.x * p.groups; base < p.rows; base += (long long)gridDim.x * p.groups) {
     const long long row = base + group;
-    const bool in = row < p.rows, ok = in && token_valid(row, p.T, p.lengths, small);
+    const bool in = row < p.rows, ok = in && token_valid(row, p.T, p.lengths);
     float x[E], dh[E], dx[E], y[E], s[N];
     load_row<E, VEC>(static_cast<const X*>(p.x) + row * D, gt, tpr, D, ok, x);
     load_row<E, VEC>(static_cast<const A*>(p.dh) + row * D, gt, tpr, D, ok, dh);

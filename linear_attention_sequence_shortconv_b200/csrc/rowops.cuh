@@ -48,16 +48,31 @@ __device__ __forceinline__ void zero8(float (&x)[8]) {
   for (int e = 0; e < 8; ++e) x[e] = 0.f;
 }
 
-// a / b for 0 <= a: in 32 bits where a fits (`small`, the same for the whole grid)
-__device__ __forceinline__ long long div_row(long long a, int b, bool small) {
-  return small ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
+// Division by an invariant integer 1 <= d < 2^31 as a multiplication (Granlund and Montgomery,
+// "Division by Invariant Integers using Multiplication", 1994, figure 4.1): with
+// l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d = (t + (n - t) / 2) / 2^(l - 1)
+// where t = m n / 2^32.  Dividends of 2^32 and more take the plain division.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() : d(1), mul(1), shift(0) {}
+  explicit FastDiv(int divisor) : d((uint32_t)divisor), shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t div32(uint32_t n) const {
+    const uint32_t t = __umulhi(mul, n);
+    return shift ? (t + ((n - t) >> 1)) >> (shift - 1) : n;
+  }
+  __device__ __forceinline__ long long div(long long n) const {
+    return n >> 32 ? n / d : (long long)div32((uint32_t)n);
+  }
+};
 
 // Whether token n = b T + t of a right-padded batch is a valid step (t < lengths[b]).
-__device__ __forceinline__ bool token_valid(long long n, int T, const int32_t* lengths, bool small) {
+__device__ __forceinline__ bool token_valid(long long n, const FastDiv& T, const int32_t* lengths) {
   if (!lengths) return true;
-  const long long b = div_row(n, T, small);
-  return n - b * T < __ldg(lengths + b);
+  const long long b = T.div(n);
+  return n - b * T.d < __ldg(lengths + b);
 }
 
 // out[v][c] = sum over blocks of part[block][v][c], v < 3 vectors of width D, in a fixed order.
@@ -79,7 +94,7 @@ struct GatedNormParams {
   void* d_gate;
   float* part;   // backward: [blocks, d] column sums
   long long rows, gate_stride;
-  int T, H;
+  FastDiv T, H;
   float eps;
 };
 
@@ -97,7 +112,8 @@ struct BlockNormParams {
   void* h;             // forward: h; backward: dy
   float* part;         // backward: [blocks, nvec, D] column sums (weight, then post_weight, then scale)
   long long rows;
-  int T, D, tpr, groups;
+  FastDiv T;
+  int D, tpr, groups;
   float res_scale, eps;
 };
 

@@ -54,7 +54,11 @@ CASES = [
     (5, 1024, 700, 100, "fp32", "bf16", 64, "runs", None),
     (3, 333, 90, 2049, "fp32", "bf16", 32, "zipf", [333, 100, 333]),
     (1, 50, 60, 8192, "bf16", "bf16", 64, "zipf", None),
-    (1, 200001, 3000, 16, "fp32", "bf16", 32, "zipf", None),       # long: more pairs per sorting block
+    (1, 16385, 3000, 16, "fp32", "bf16", 32, "zipf", None),        # more than one pair per thread of the sort
+    (8, 16384, 1 << 20, 8, "fp32", "fp32", 64, "zipf", [16384] * 7 + [5]),  # the longest batch sorted in one launch
+    (1, 200001, 3000, 16, "fp32", "bf16", 32, "zipf", None),       # longer: sorted by tiles
+    (3, 100000, 1 << 20, 8, "fp32", "bf16", 64, "zipf", [100000, 1, 77777]),
+    (1, 300000, 1, 8, "bf16", "bf16", 32, "one", None),
 ]
 
 
