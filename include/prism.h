@@ -396,7 +396,7 @@ int prism_gated_norm_fwd(const void* o, const void* gate, const float* weight, c
  * prism_gated_norm_bwd - gradients of <y, dy>:  d_o, d_gate (dense; NULL iff gate is NULL)
  * [B,T,H,d] dtype and d_weight [d] fp32.  d_o may be dy; it is what prism_scan_bwd takes as dO.
  * The statistics are computed again from o.  workspace: at least
- * prism_gated_norm_bwd_workspace_size() bytes.  Two launches.
+ * prism_gated_norm_bwd_workspace_size() bytes.  Two launches, or one for few rows.
  */
 size_t prism_gated_norm_bwd_workspace_size(int B, int T, int H, int d);
 
@@ -428,7 +428,7 @@ int prism_block_norm_fwd(const void* x, const void* y, const float* post_weight,
  *   dh [B,T,D] dtype; dx_out [B,T,D] x_dtype or NULL (zero)
  *   dx [B,T,D] x_dtype, may be dx_out; dy [B,T,D] dtype (NULL iff y is NULL)
  *   d_weight, and where their vectors are given d_post_weight and d_scale: [D] fp32
- * workspace: at least prism_block_norm_bwd_workspace_size() bytes.  Two launches.
+ * workspace: at least prism_block_norm_bwd_workspace_size() bytes.  Two launches, or one for few rows.
  */
 size_t prism_block_norm_bwd_workspace_size(int B, int T, int D);
 
@@ -455,8 +455,9 @@ int prism_embed_fwd(const void* ids, const void* table, const int32_t* lengths, 
  *   accumulate 0: every row of d_table is written (zero where no token names it); otherwise
  *   the sums are added to what d_table holds and only the rows that a token names are touched
  * Ids outside [0, V) give no gradient and are recorded as in prism_embed_fwd.  workspace: at
- * least prism_embed_bwd_workspace_size() bytes (16 bytes a token for the sorted ids, 8 to 64 KB
- * of counts and 8 D bytes for each of about 2048 runs of tokens).  Four to six launches.
+ * least prism_embed_bwd_workspace_size() bytes (16 bytes a token for the sorted ids, up to 2 MB
+ * of counts, and 8 D bytes for each chunk of 16 to 128 tokens).  Three launches for up to 32768
+ * tokens, else five to nine.
  */
 size_t prism_embed_bwd_workspace_size(int B, int T, int V, int D);
 

@@ -71,11 +71,6 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(EmbedParams p, i
 constexpr int kMaxBins = 1 << kEmbedMaxDigit;
 constexpr uint32_t kNoKey = 0xffffffffu;  // a place behind the last token
 
-// Programmatic launch of the next kernel of the chain: it may start once every block of this one
-// has said so, and waits for this one's end before it reads its results.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Stable ranks of a warp's 32 * KPT consecutive keys among the equal digits of the warp, and
 // the warp's counts per digit (`count`, zero before).  The lanes of equal digit are found by one
 // vote per bit.
@@ -671,23 +666,6 @@ cudaError_t sort_cluster(const EmbedParams& p, const EmbedPlan& plan, cudaStream
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, sort_cluster_kernel<I, KPT>, p, plan);
-}
-
-// A launch that may overlap the end of the one before it (whose results its kernel waits for).
-template <typename... Args>
-cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                           Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <typename I, int KPT>

@@ -12,12 +12,10 @@
 namespace prism {
 int device_setup(int** status_out);
 int gated_norm_bwd_blocks(long long rows, int d);
-int block_norm_blocks(long long rows, int D, bool bwd);
+int block_norm_blocks(long long rows, int D, bool bwd, int x_bytes, int bytes);
 cudaError_t launch_gated_norm_fwd(const GatedNormParams& p, int d, int gate, int dtype, cudaStream_t stream);
-cudaError_t launch_gated_norm_bwd(const GatedNormParams& p, int d, int gate, int dtype, float* d_weight,
-                                  cudaStream_t stream);
-cudaError_t launch_block_norm(const BlockNormParams& p, bool bwd, int x_dtype, int dtype, float* const (&sums)[3],
-                              cudaStream_t stream);
+cudaError_t launch_gated_norm_bwd(const GatedNormParams& p, int d, int gate, int dtype, cudaStream_t stream);
+cudaError_t launch_block_norm(const BlockNormParams& p, bool bwd, int x_dtype, int dtype, cudaStream_t stream);
 cudaError_t launch_embed_fwd(const EmbedParams& p, int ids_bits, int table_dtype, int dtype, cudaStream_t stream);
 cudaError_t launch_embed_bwd(const EmbedParams& p, int ids_bits, int dtype, cudaStream_t stream);
 cudaError_t launch_adamw(const AdamTensor* tensors, int count, unsigned blocks, const AdamParams& a, int p_dtype,
@@ -117,8 +115,9 @@ int prism_gated_norm_fwd(const void* o, const void* gate, const float* weight, c
   int* status = nullptr;
   rc = prism::device_setup(&status);
   if (rc != PRISM_OK) return rc;
-  const prism::GatedNormParams p{o, gate, weight, nullptr, lengths, y, nullptr, nullptr, (long long)toks * H,
-                                 gate_stride, prism::FastDiv(T), prism::FastDiv(H), eps};
+  const prism::GatedNormParams p{o, gate, weight, nullptr, lengths, y, nullptr, nullptr, nullptr, (long long)toks * H,
+                                 gate_stride, prism::FastDiv(T), prism::FastDiv(H), eps,
+                                 lengths || (gate && gate_stride != (long long)H * d)};
   return launched(prism::launch_gated_norm_fwd(p, d, gate_kind(gate, act), dtype, cuda_stream(stream)));
 }
 
@@ -147,8 +146,9 @@ int prism_gated_norm_bwd(const void* o, const void* gate, const float* weight, c
   rc = prism::device_setup(&status);
   if (rc != PRISM_OK) return rc;
   const prism::GatedNormParams p{o, gate, weight, dy, lengths, d_o, d_gate, static_cast<float*>(workspace),
-                                 (long long)toks * H, gate_stride, prism::FastDiv(T), prism::FastDiv(H), eps};
-  return launched(prism::launch_gated_norm_bwd(p, d, gate_kind(gate, act), dtype, d_weight, cuda_stream(stream)));
+                                 d_weight, (long long)toks * H, gate_stride, prism::FastDiv(T), prism::FastDiv(H), eps,
+                                 lengths || (gate && gate_stride != (long long)H * d)};
+  return launched(prism::launch_gated_norm_bwd(p, d, gate_kind(gate, act), dtype, cuda_stream(stream)));
 }
 
 int prism_block_norm_fwd(const void* x, const void* y, const float* post_weight, const float* scale,
@@ -167,14 +167,17 @@ int prism_block_norm_fwd(const void* x, const void* y, const float* post_weight,
   rc = prism::device_setup(&status);
   if (rc != PRISM_OK) return rc;
   const prism::BlockNormParams p{x, y, post_weight, scale, weight, nullptr, nullptr, lengths, x_out, h, nullptr,
-                                 (long long)B * T, prism::FastDiv(T), D, 0, 0, res_scale, eps};
-  float* const sums[3] = {nullptr, nullptr, nullptr};
-  return launched(prism::launch_block_norm(p, false, x_dtype, dtype, sums, cuda_stream(stream)));
+                                 {nullptr, nullptr, nullptr}, (long long)B * T, prism::FastDiv(T), D, 0, 0, res_scale, eps, 1.f / D};
+  return launched(prism::launch_block_norm(p, false, x_dtype, dtype, cuda_stream(stream)));
 }
 
 size_t prism_block_norm_bwd_workspace_size(int B, int T, int D) {
   if (check_block(B, T, D, 1.f, 1.f, PRISM_BF16, PRISM_BF16) != PRISM_OK) return 0;
-  return round256((size_t)prism::block_norm_blocks((long long)B * T, D, true) * 3 * D * 4);
+  int blocks = 0;  // the most of all types
+  for (int x_bytes = 2; x_bytes <= 4; x_bytes += 2)
+    for (int bytes = 2; bytes <= x_bytes; bytes += 2)
+      blocks = std::max(blocks, prism::block_norm_blocks((long long)B * T, D, true, x_bytes, bytes));
+  return round256((size_t)blocks * 3 * D * 4);
 }
 
 int prism_block_norm_bwd(const void* x_out, const void* y, const float* post_weight, const float* scale,
@@ -200,9 +203,9 @@ int prism_block_norm_bwd(const void* x_out, const void* y, const float* post_wei
   rc = prism::device_setup(&status);
   if (rc != PRISM_OK) return rc;
   const prism::BlockNormParams p{x_out, y, post_weight, scale, weight, dh, dx_out, lengths, dx, dy,
-                                 static_cast<float*>(workspace), (long long)B * T, prism::FastDiv(T), D, 0, 0, res_scale, eps};
-  float* const sums[3] = {d_weight, d_post_weight, d_scale};
-  return launched(prism::launch_block_norm(p, true, x_dtype, dtype, sums, cuda_stream(stream)));
+                                 static_cast<float*>(workspace),
+                                 {d_weight, post_weight ? d_post_weight : d_scale, d_scale}, (long long)B * T, prism::FastDiv(T), D, 0, 0, res_scale, eps, 1.f / D};
+  return launched(prism::launch_block_norm(p, true, x_dtype, dtype, cuda_stream(stream)));
 }
 
 int prism_embed_fwd(const void* ids, const void* table, const int32_t* lengths, int B, int T, int V, int D,

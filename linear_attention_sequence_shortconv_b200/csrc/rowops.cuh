@@ -48,6 +48,146 @@ __device__ __forceinline__ void zero8(float (&x)[8]) {
   for (int e = 0; e < 8; ++e) x[e] = 0.f;
 }
 
+// Two fp32 operations in one instruction (sm_100a's packed forms): these kernels issue several
+// operations per loaded byte, so that their rate would be the limit otherwise.
+__device__ __forceinline__ unsigned long long bits2(float2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 float2_of(unsigned long long r) {
+  float2 a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+  return a;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return float2_of(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w) {  // a bf16 is the upper half of the fp32 of the same value
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// How W neighbouring threads share 8 W consecutive elements.  Thread l holds eight: in 16-bit
+// rows elements 8 l .. 8 l + 7 (16 bytes), else 4 l .. 4 l + 3 and 4 W + 4 l .. 4 W + 4 l + 3, so
+// that every access of the threads is to consecutive bytes (a thread that took the two halves
+// of a 32-byte sector in turn would have it moved twice).
+template <bool WIDE>  // WIDE: fp32 rows among them
+__device__ __forceinline__ int share(int e, int l, int W) {
+  return WIDE ? e / 4 * 4 * W + 4 * l + e % 4 : 8 * l + e;
+}
+
+// Eight elements of a thread as loaded, and as pairs of fp32 numbers.
+template <typename T>
+struct Raw8 {
+  static constexpr int kPieces = (int)sizeof(T) / 2;  // of 16 bytes
+  uint4 v[kPieces];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int h = 0; h < kPieces; ++h) v[h] = make_uint4(0, 0, 0, 0);
+  }
+  // row: the first of the 8 W elements
+  template <bool WIDE>
+  __device__ __forceinline__ void load(const T* row, int l, int W) {
+    if (sizeof(T) == 2 && WIDE) {
+      const uint2 a = __ldcs(reinterpret_cast<const uint2*>(row + share<true>(0, l, W)));
+      const uint2 b = __ldcs(reinterpret_cast<const uint2*>(row + share<true>(4, l, W)));
+      v[0] = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+#pragma unroll
+      for (int h = 0; h < kPieces; ++h) v[h] = __ldcs(reinterpret_cast<const uint4*>(row + share<WIDE>(4 * h, l, W)));
+    }
+  }
+  __device__ __forceinline__ float2 get(int i) const {  // i: a constant after unrolling
+    const uint4 q = v[sizeof(T) == 4 ? i / 2 % kPieces : 0];
+    if (sizeof(T) == 4)
+      return i & 1 ? make_float2(__uint_as_float(q.z), __uint_as_float(q.w))
+                   : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+    return unpack_bf16(i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w);
+  }
+};
+
+// Eight elements of a thread into row[0 .. 8 W), of which the first n exist.
+template <bool WIDE>
+__device__ __forceinline__ void store_shared8(float* row, int l, int W, int n, const float2 (&x)[4]) {
+  static_assert(WIDE, "fp32 rows");
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int e = share<true>(4 * h, l, W);
+    if (e < n) *reinterpret_cast<float4*>(row + e) = make_float4(x[2 * h].x, x[2 * h].y, x[2 * h + 1].x, x[2 * h + 1].y);
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store_shared8(__nv_bfloat16* row, int l, int W, int n, const float2 (&x)[4]) {
+  const uint4 v = make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y), pack_bf16(x[2].x, x[2].y),
+                             pack_bf16(x[3].x, x[3].y));
+  if (WIDE) {
+    const int a = share<true>(0, l, W), b = share<true>(4, l, W);
+    if (a < n) *reinterpret_cast<uint2*>(row + a) = make_uint2(v.x, v.y);
+    if (b < n) *reinterpret_cast<uint2*>(row + b) = make_uint2(v.z, v.w);
+  } else if (8 * l < n) {
+    *reinterpret_cast<uint4*>(row + 8 * l) = v;
+  }
+}
+
+// A ring of `STAGES` sets of N 16-byte pieces in shared memory, private to a thread: the thread
+// copies what it will read itself (asynchronously), so that the copies of the next STAGES - 1
+// sets are in flight without registers and no thread waits for another.  A set is filled again
+// only after the thread has used the values that it read from it.
+template <int N, int STAGES>
+struct Ring {
+  uint4* base;  // this thread's first slot; consecutive threads have consecutive slots
+  int threads, stage;
+  __device__ __forceinline__ Ring(void* smem)
+      : base(static_cast<uint4*>(smem) + threadIdx.x), threads(blockDim.x), stage(0) {}
+  static __host__ __device__ constexpr size_t bytes(int threads) { return (size_t)STAGES * N * 16 * threads; }
+  // Eight of the elements row[0 .. 8 W) into the pieces from `at` on of the set that lies `ahead`
+  // sets behind the next one to be read.  Only the first n elements of the row exist; the
+  // others become zero, and `any` (readable) stands for their address.
+  template <bool WIDE, typename T>
+  __device__ __forceinline__ void copy(int ahead, int at, const T* row, int l, int W, int n, const void* any) {
+    int s = stage + ahead;
+    s = s >= STAGES ? s - STAGES : s;
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(base + (s * N + at) * threads);
+#pragma unroll
+    for (int h = 0; h < (WIDE ? 2 : 1); ++h) {
+      const int e = share<WIDE>(4 * h, l, W);
+      const bool ok = e < n;
+      const void* src = ok ? row + e : any;
+      if (sizeof(T) == 2 && WIDE)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + 8 * h), "l"(src), "r"(ok ? 8 : 0)
+                     : "memory");
+      else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * h * threads), "l"(src),
+                     "r"(ok ? 16 : 0) : "memory");
+    }
+  }
+  __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // the next set is complete (one commit per set, in order)
+  __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory"); }
+  __device__ __forceinline__ void drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+  template <typename T>
+  __device__ __forceinline__ Raw8<T> read(int at) const {
+    Raw8<T> r;
+#pragma unroll
+    for (int h = 0; h < Raw8<T>::kPieces; ++h) r.v[h] = base[(stage * N + at + h) * threads];
+    return r;
+  }
+  __device__ __forceinline__ void advance() { stage = stage + 1 == STAGES ? 0 : stage + 1; }
+};
+
 // Division by an invariant integer 1 <= d < 2^31 as a multiplication (Granlund and Montgomery,
 // "Division by Invariant Integers using Multiplication", 1994, figure 4.1): with
 // l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d = (t + (n - t) / 2) / 2^(l - 1)
@@ -75,6 +215,28 @@ __device__ __forceinline__ bool token_valid(long long n, const FastDiv& T, const
   return n - b * T.d < __ldg(lengths + b);
 }
 
+// Programmatic launch of the next kernel of a chain: it may start once every block of this one
+// has said so, and waits for this one's end before it reads its results.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A launch that may overlap the end of the one before it (whose results its kernel waits for).
+template <typename... Args>
+cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                           Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // out[v][c] = sum over blocks of part[block][v][c], v < 3 vectors of width D, in a fixed order.
 struct ColumnSumParams {
   const float* part;  // [blocks, nvec, D]
@@ -93,9 +255,11 @@ struct GatedNormParams {
   void* y;       // forward: y; backward: d_o
   void* d_gate;
   float* part;   // backward: [blocks, d] column sums
+  float* d_weight;
   long long rows, gate_stride;
   FastDiv T, H;
   float eps;
+  bool by_token;  // rows are found by their tokens: a strided gate, or lengths
 };
 
 // Pointers and sizes of one block norm call, forward or backward (device pointers).
@@ -110,11 +274,12 @@ struct BlockNormParams {
   const int32_t* lengths;
   void* x_out;         // forward: x'; backward: dx
   void* h;             // forward: h; backward: dy
-  float* part;         // backward: [blocks, nvec, D] column sums (weight, then post_weight, then scale)
+  float* part;         // backward: [blocks, nvec, D] column sums of the vectors' gradients
+  float* sums[3];      // the gradients of weight, then of post_weight and scale as far as given
   long long rows;
   FastDiv T;
   int D, tpr, groups;
-  float res_scale, eps;
+  float res_scale, eps, inv_D;
 };
 
 }  // namespace prism

@@ -8,13 +8,14 @@ caller orders the stream behind the work that made the inputs.
 from __future__ import annotations
 
 import contextlib
-import ctypes
+import itertools
 import struct
 from typing import Dict, List, Optional, Sequence, Union
 
 import torch
 
-from ._lib import _ptr, PRISM_BF16, PRISM_FP32, PrismError, _call_device, _check, _dtype_code, lib
+from ._lib import PRISM_BF16, PRISM_FP32, PrismError, _call_device, _dtype_code, lib
+from ._lib import _check as _check_slow
 
 PRISM_ACT_SILU = 0
 PRISM_ACT_SIGMOID = 1
@@ -28,6 +29,21 @@ def _act_code(act: str) -> int:
     return ACTS[act]
 
 
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _check(t, name, dtype=None, required=True, shape=None, device=None):
+    """The mixer's check of one tensor argument, with a short way for a tensor that is fine."""
+    if (t is not None and t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype == dtype)
+            and (shape is None or t.shape == shape) and (device is None or t.device == device)):
+        return
+    _check_slow(t, name, dtype, required, shape, device)
+
+
+_STAY = contextlib.nullcontext()
+
+
 def _on(dev: torch.device, stream, tensors=()):
     """Context in which a call allocates and launches: the tensors' device, and `stream` where
     the caller names one (its inputs are then kept until the stream is through with them)."""
@@ -36,13 +52,13 @@ def _on(dev: torch.device, stream, tensors=()):
             if t is not None:
                 t.record_stream(stream)
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() == dev.index:
-        return contextlib.nullcontext()
+    if torch._C._cuda_getDevice() == dev.index:
+        return _STAY
     return torch.cuda.device(dev)
 
 
 def _here(dev: torch.device):
-    return torch.cuda.current_stream(dev).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _done(rc: int, what: str) -> None:
@@ -302,15 +318,17 @@ def adamw_state(params: Sequence[torch.Tensor], bits: int = 32) -> Dict[str, Lis
 def _list_checks(tensors, name, dtype, params, dev, shapes=True):
     if len(tensors) != len(params):
         raise ValueError(f"{name} must have {len(params)} tensors, got {len(tensors)}")
+    at = dev.index
     for t, p in zip(tensors, params):
+        if t.dtype == dtype and t.get_device() == at and t.is_contiguous() and (not shapes or t.shape == p.shape):
+            continue
         if t.dtype != dtype:
             raise TypeError(f"{name} must all be {dtype}, got {t.dtype}")
         if t.device != dev:
             raise ValueError(f"{name} holds a tensor on {t.device}, but the call's tensors are on {dev}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if shapes and t.shape != p.shape:
-            raise ValueError(f"{name} must have the parameters' shapes, got {tuple(t.shape)} for {tuple(p.shape)}")
+        raise ValueError(f"{name} must have the parameters' shapes, got {tuple(t.shape)} for {tuple(p.shape)}")
 
 
 def _scalar(x, name, dtype, dev):
@@ -354,7 +372,6 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     _list_checks(grads, "grads", grads[0].dtype, params, dev)
     _list_checks(exp_avg, "exp_avg", state_dtype, params, dev)
     _list_checks(exp_avg_sq, "exp_avg_sq", state_dtype, params, dev)
-    none = [None] * n
     if bits == 8:
         if exp_avg_scale is None or exp_avg_sq_scale is None:
             raise ValueError("8-bit states need exp_avg_scale and exp_avg_sq_scale")
@@ -383,15 +400,19 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
             raise TypeError("grad_scale must be a CUDA tensor")
     else:
         grad_scale_dev = None
-    fields: list = []
-    for p, g, m, v, ms, vs, c, wd in zip(params, grads, exp_avg, exp_avg_sq, exp_avg_scale or none,
-                                         exp_avg_sq_scale or none, copies or none, decay):
-        fields += (p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), 0 if ms is None else ms.data_ptr(),
-                   0 if vs is None else vs.data_ptr(), 0 if c is None else c.data_ptr(), p.numel(), wd)
-    table = struct.pack("@" + "7PQd" * n, *fields)  # an array of prism_adamw_tensor
-    used = (*params, *grads, *exp_avg, *exp_avg_sq, *(exp_avg_scale or ()), *(exp_avg_sq_scale or ()),
-            *(copies or ()), *(x for x in (step, lr, grad_scale) if isinstance(x, torch.Tensor)))
-    with _on(dev, stream, used if stream is not None else ()):
+    zeros = [0] * n
+
+    def pointers(tensors):
+        return zeros if tensors is None else [t.data_ptr() for t in tensors]
+
+    rows = zip(pointers(params), pointers(grads), pointers(exp_avg), pointers(exp_avg_sq), pointers(exp_avg_scale),
+               pointers(exp_avg_sq_scale), pointers(copies), [p.numel() for p in params], decay)
+    table = struct.pack("@" + "7PQd" * n, *itertools.chain.from_iterable(rows))  # an array of prism_adamw_tensor
+    used = ()
+    if stream is not None:
+        used = (*params, *grads, *exp_avg, *exp_avg_sq, *(exp_avg_scale or ()), *(exp_avg_sq_scale or ()),
+                *(copies or ()), *(x for x in (step, lr, grad_scale) if isinstance(x, torch.Tensor)))
+    with _on(dev, stream, used):
         _done(lib().prism_adamw_step(table, n, 0 if step_host is None else int(step_host), step_dev,
                                      0.0 if lr_host is None else float(lr_host), lr_dev, betas[0], betas[1], eps,
                                      grad_scale_dev, p_code, g_code, bits, _here(dev)), "prism_adamw_step")
