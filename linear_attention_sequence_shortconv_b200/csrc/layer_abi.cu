@@ -354,11 +354,14 @@ int prism_adamw_step(const prism_adamw_tensor* tensors, int count, int step, con
     a.b2 = (float)beta2;
     a.r2 = (float)(1.0 - beta2);
     a.eps = (float)eps;
+    long long elements = 0;
+    for (int i = 0; i < used; ++i) elements += list[i].n;
+    a.chunk = prism::adam_chunk(elements, state_bits);
     // as many tensors per launch as the parameters and the grid hold
     int first = 0;
     long long blocks = 0;
     for (int i = 0; i <= used && rc == PRISM_OK; ++i) {
-      const long long more = i < used ? (list[i].n + prism::kAdamChunk - 1) / prism::kAdamChunk : 0;
+      const long long more = i < used ? (list[i].n + a.chunk - 1) / a.chunk : 0;
       if (i == used || i - first == prism::kAdamMostTensors || (i > first && blocks + more > 0x7fffffffll)) {
         rc = launched(prism::launch_adamw(list + first, i - first, (unsigned)blocks, a, p_dtype, g_dtype, state_bits,
                                           cuda_stream(stream)));

@@ -110,6 +110,17 @@ struct Raw8 {
       for (int h = 0; h < kPieces; ++h) v[h] = __ldcs(reinterpret_cast<const uint4*>(row + share<WIDE>(4 * h, l, W)));
     }
   }
+  // from fp32 values (exact where they came from a T)
+  __device__ __forceinline__ void put(const float (&x)[8]) {
+    if (sizeof(T) == 2) {
+      v[0] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    } else {
+#pragma unroll
+      for (int h = 0; h < kPieces; ++h)
+        v[h] = make_uint4(__float_as_uint(x[4 * h % 8]), __float_as_uint(x[(4 * h + 1) % 8]),
+                          __float_as_uint(x[(4 * h + 2) % 8]), __float_as_uint(x[(4 * h + 3) % 8]));
+    }
+  }
   __device__ __forceinline__ float2 get(int i) const {  // i: a constant after unrolling
     const uint4 q = v[sizeof(T) == 4 ? i / 2 % kPieces : 0];
     if (sizeof(T) == 4)
