@@ -499,6 +499,36 @@ int prism_adamw_step(const prism_adamw_tensor* tensors, int count, int step, con
                      const float* lr_dev, double beta1, double beta2, double eps, const float* grad_scale,
                      int p_dtype, int g_dtype, int state_bits, prism_stream_t stream);
 
+/* A tensor as DLPack describes it (the layout of DLTensor, DLPack 1). */
+typedef struct prism_dl_tensor {
+  void* data;
+  int32_t device_type; /* 2: CUDA */
+  int32_t device_id;
+  int32_t ndim;
+  uint8_t type_code; /* 2: float, 4: bfloat, 10: e4m3 (fn) */
+  uint8_t type_bits;
+  uint16_t type_lanes;
+  int64_t* shape;
+  int64_t* strides; /* NULL: dense */
+  uint64_t byte_offset;
+} prism_dl_tensor;
+
+/* DLPack's exchange function of a framework: views `object` as a tensor; 0 on success. */
+typedef int (*prism_dl_from_object)(void* object, prism_dl_tensor* out);
+
+/*
+ * prism_dl_pointers - the data pointers of n objects of a framework, for the host arrays of
+ * prism_adamw_step (host only, no CUDA call; a binding's loop over hundreds of tensors).
+ * views[i] is what from_object says of objects[i].  The object has to be a dense tensor of the
+ * type on CUDA device `device`; with `like`, of like[i]'s shape (block 0) or of as many
+ * elements as like[i] has blocks of `block`.  Its pointer goes to out + i * stride, its number
+ * of elements (a long long) to count + i * stride where count is given.
+ * Returns n, or the index of the first object that is not as described.
+ */
+int prism_dl_pointers(int n, void* const* objects, prism_dl_from_object from_object, int device, int type_code,
+                      int type_bits, const prism_dl_tensor* like, int block, prism_dl_tensor* views, void* out,
+                      void* count, size_t stride);
+
 /* Synchronises `stream`, then returns and clears the device status word of the
  * current device: PRISM_OK, PRISM_ERR_TIMEOUT, PRISM_ERR_BOUNDS, or
  * PRISM_ERR_CUDA if the synchronisation itself failed. */

@@ -55,6 +55,7 @@ EXPORTS = (
     "prism_embed_bwd",
     "prism_embed_bwd_workspace_size",
     "prism_adamw_step",
+    "prism_dl_pointers",
     "prism_scan_fwd_uses_tensor_cores",
     "prism_scan_fwd_launches",
     "prism_scan_fwd_split_chunks",
@@ -135,6 +136,7 @@ def lib() -> ctypes.CDLL:
     L.prism_embed_bwd.restype = ci
     L.prism_adamw_step.argtypes = [vp, ci, ci, i32p, cd, fp, cd, cd, cd, fp, ci, ci, ci, vp]
     L.prism_adamw_step.restype = ci
+    L.prism_dl_pointers.restype = ci
     L.prism_scan_fwd_uses_tensor_cores.argtypes = [ci] * 6
     L.prism_scan_fwd_uses_tensor_cores.restype = ci
     L.prism_scan_fwd_launches.argtypes = [ci] * 9

@@ -378,4 +378,35 @@ int prism_adamw_step(const prism_adamw_tensor* tensors, int count, int step, con
   return rc;
 }
 
+int prism_dl_pointers(int n, void* const* objects, prism_dl_from_object from_object, int device, int type_code,
+                      int type_bits, const prism_dl_tensor* like, int block, prism_dl_tensor* views, void* out,
+                      void* count, size_t stride) {
+  for (int i = 0; i < n; ++i) {
+    prism_dl_tensor& v = views[i];
+    if (from_object(objects[i], &v) != 0) return i;
+    if (v.device_type != 2 || v.device_id != device || v.type_code != type_code || v.type_bits != type_bits ||
+        v.type_lanes != 1)
+      return i;
+    long long elements = 1;
+    for (int d = 0; d < v.ndim; ++d) elements *= v.shape[d];
+    long long step = 1;  // dense, as far as it matters: the stride of a dimension of one element does not
+    for (int d = v.ndim - 1; d >= 0 && v.strides && elements > 0; --d) {
+      if (v.shape[d] != 1 && v.strides[d] != step) return i;
+      step *= v.shape[d];
+    }
+    if (like && block > 0) {
+      long long of = 1;
+      for (int d = 0; d < like[i].ndim; ++d) of *= like[i].shape[d];
+      if (elements != (of + block - 1) / block) return i;
+    } else if (like) {
+      if (v.ndim != like[i].ndim) return i;
+      for (int d = 0; d < v.ndim; ++d)
+        if (v.shape[d] != like[i].shape[d]) return i;
+    }
+    *reinterpret_cast<void**>(static_cast<char*>(out) + i * stride) = static_cast<char*>(v.data) + v.byte_offset;
+    if (count) *reinterpret_cast<long long*>(static_cast<char*>(count) + i * stride) = elements;
+  }
+  return n;
+}
+
 }  // extern "C"

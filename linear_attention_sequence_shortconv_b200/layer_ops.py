@@ -7,14 +7,15 @@ caller orders the stream behind the work that made the inputs.
 """
 from __future__ import annotations
 
+import array
 import contextlib
-import itertools
-import struct
+import ctypes
+import functools
 from typing import Dict, List, Optional, Sequence, Union
 
 import torch
 
-from ._lib import PRISM_BF16, PRISM_FP32, PrismError, _call_device, _dtype_code, lib
+from ._lib import LIB_PATH, PRISM_BF16, PRISM_FP32, PrismError, _call_device, _dtype_code, lib
 from ._lib import _check as _check_slow
 
 PRISM_ACT_SILU = 0
@@ -88,14 +89,14 @@ def _gate_stride(gate, o, sizes) -> int:
     B, T, H, d = sizes
     if gate is None:
         return H * d
+    if gate.shape == o.shape and gate.dtype == o.dtype and gate.device == o.device and gate.is_contiguous():
+        return H * d
     if not gate.is_cuda or gate.device != o.device:
         raise ValueError(f"gate is on {gate.device}, but the call's tensors are on {o.device}")
     if gate.dtype != o.dtype:
         raise TypeError(f"gate must be {o.dtype}, got {gate.dtype}")
     if gate.shape != o.shape:
         raise ValueError(f"gate must have shape {tuple(o.shape)}, got {tuple(gate.shape)}")
-    if gate.is_contiguous():
-        return H * d
     st = gate.stride()
     step = st[-3] if T > 1 or gate.dim() == 3 else st[0]
     if B * T == 1:
@@ -341,6 +342,68 @@ def _scalar(x, name, dtype, dev):
     return None, _ptr(x)
 
 
+_ADAMW_TENSOR = 72  # bytes of prism_adamw_tensor: seven pointers, a count and a double
+_DL_TENSOR = 48      # bytes of prism_dl_tensor
+_DL_TYPES = {torch.float32: (2, 32), torch.bfloat16: (4, 16), torch.float8_e4m3fn: (10, 8)}
+
+
+@functools.lru_cache(maxsize=None)
+def _dl_exchange():
+    """(prism_dl_pointers, torch's DLPack exchange function), or None where torch has none.  The
+    function runs with the interpreter's lock held, since it looks at Python objects."""
+    capsule = getattr(torch.Tensor, "__dlpack_c_exchange_api__", None)
+    if capsule is None:
+        return None
+    get = ctypes.pythonapi.PyCapsule_GetPointer
+    get.restype, get.argtypes = ctypes.c_void_p, [ctypes.py_object, ctypes.c_char_p]
+    api = get(capsule, b"dlpack_exchange_api")
+    # DLPackExchangeAPI: the version (two 32-bit numbers), an older table, then the functions; the
+    # one that views an object as a tensor is the fourth
+    if (ctypes.c_uint32 * 1).from_address(api)[0] != 1:
+        return None
+    view = (ctypes.c_void_p * 4).from_address(api + 16)[3]
+    if not view:
+        return None
+    gather = ctypes.PyDLL(LIB_PATH).prism_dl_pointers
+    vp, ci = ctypes.c_void_p, ctypes.c_int
+    gather.restype = ci
+    gather.argtypes = [ci, vp, vp, ci, ci, ci, vp, ci, vp, vp, vp, ctypes.c_size_t]
+    return gather, view
+
+
+def _adamw_table(n, lists, decay, dev):
+    """The host array of prism_adamw_tensor of a step, its tensors checked."""
+    table = ctypes.create_string_buffer(_ADAMW_TENSOR * n)
+    memoryview(table).cast("B").cast("d")[8::9] = memoryview(decay)
+    at = ctypes.addressof(table)
+    exchange = _dl_exchange()
+    if exchange is not None:
+        gather, view = exchange
+        first, views = ctypes.create_string_buffer(_DL_TENSOR * n), ctypes.create_string_buffer(_DL_TENSOR * n)
+        objects = ctypes.c_void_p * n
+        for field, (_, tensors, dtype, blocks) in enumerate(lists):
+            if tensors is None:
+                continue
+            code, bits = _DL_TYPES[dtype]
+            if gather(n, objects(*map(id, tensors)), view, dev.index, code, bits, None if field == 0 else first,
+                      STATE_BLOCK if blocks else 0, first if field == 0 else views, at + 8 * field,
+                      at + 56 if field == 0 else None, _ADAMW_TENSOR) != n:
+                break  # the checks below say which and why
+        else:
+            return table
+    fields = memoryview(table).cast("B").cast("Q")
+    params = lists[0][1]
+    for field, (name, tensors, dtype, blocks) in enumerate(lists):
+        if tensors is None:
+            continue
+        _list_checks(tensors, name, dtype, params, dev, shapes=not blocks)
+        if blocks and any(s.numel() != -(-p.numel() // STATE_BLOCK) for s, p in zip(tensors, params)):
+            raise ValueError(f"{name} must have one element per {STATE_BLOCK} of its parameter")
+        fields[field::9] = memoryview(array.array("Q", [t.data_ptr() for t in tensors]))
+    fields[7::9] = memoryview(array.array("Q", [p.numel() for p in params]))
+    return table
+
+
 def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], exp_avg: Sequence[torch.Tensor],
                exp_avg_sq: Sequence[torch.Tensor], step: Union[int, torch.Tensor] = 1,
                lr: Union[float, torch.Tensor] = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -356,6 +419,10 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     gradients.  ``weight_decay``: one number, or one per tensor.  ``copies``: bf16 tensors that
     receive the new fp32 parameters.  Tensors of the call must not overlap.
     """
+    # kept as they are for the length of the call
+    params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copies = (
+        x if x is None or isinstance(x, (list, tuple)) else list(x)
+        for x in (params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copies))
     n = len(params)
     if n == 0:
         return
@@ -368,28 +435,16 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     if state_dtype not in (torch.float32, torch.float8_e4m3fn):
         raise TypeError(f"exp_avg must be float32 or float8_e4m3fn, got {state_dtype}")
     bits = 32 if state_dtype == torch.float32 else 8
-    _list_checks(params, "params", params[0].dtype, params, dev)
-    _list_checks(grads, "grads", grads[0].dtype, params, dev)
-    _list_checks(exp_avg, "exp_avg", state_dtype, params, dev)
-    _list_checks(exp_avg_sq, "exp_avg_sq", state_dtype, params, dev)
-    if bits == 8:
-        if exp_avg_scale is None or exp_avg_sq_scale is None:
-            raise ValueError("8-bit states need exp_avg_scale and exp_avg_sq_scale")
-        for name, scales in (("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)):
-            _list_checks(scales, name, torch.float32, params, dev, shapes=False)
-            for s, p in zip(scales, params):
-                if s.numel() != -(-p.numel() // STATE_BLOCK):
-                    raise ValueError(f"{name} must have one element per {STATE_BLOCK} of its parameter")
-    elif exp_avg_scale is not None or exp_avg_sq_scale is not None:
+    if bits == 8 and (exp_avg_scale is None or exp_avg_sq_scale is None):
+        raise ValueError("8-bit states need exp_avg_scale and exp_avg_sq_scale")
+    if bits == 32 and (exp_avg_scale is not None or exp_avg_sq_scale is not None):
         raise ValueError("fp32 states take no scales")
-    if copies is not None:
-        if p_code != PRISM_FP32:
-            raise ValueError("copies go with fp32 parameters")
-        _list_checks(copies, "copies", torch.bfloat16, params, dev)
+    if copies is not None and p_code != PRISM_FP32:
+        raise ValueError("copies go with fp32 parameters")
     if isinstance(weight_decay, (int, float)):
-        decay = [float(weight_decay)] * n
+        decay = array.array("d", (weight_decay,)) * n
     else:
-        decay = [float(x) for x in weight_decay]
+        decay = array.array("d", weight_decay)
         if len(decay) != n:
             raise ValueError(f"weight_decay must be a number or {n} of them, got {len(decay)}")
     step_host, step_dev = _scalar(step, "step", torch.int32, dev)
@@ -400,14 +455,15 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
             raise TypeError("grad_scale must be a CUDA tensor")
     else:
         grad_scale_dev = None
-    zeros = [0] * n
-
-    def pointers(tensors):
-        return zeros if tensors is None else [t.data_ptr() for t in tensors]
-
-    rows = zip(pointers(params), pointers(grads), pointers(exp_avg), pointers(exp_avg_sq), pointers(exp_avg_scale),
-               pointers(exp_avg_sq_scale), pointers(copies), [p.numel() for p in params], decay)
-    table = struct.pack("@" + "7PQd" * n, *itertools.chain.from_iterable(rows))  # an array of prism_adamw_tensor
+    # the tensors in the order of prism_adamw_tensor's fields, with their types
+    lists = [("params", params, params[0].dtype, False), ("grads", grads, grads[0].dtype, False),
+             ("exp_avg", exp_avg, state_dtype, False), ("exp_avg_sq", exp_avg_sq, state_dtype, False),
+             ("exp_avg_scale", exp_avg_scale, torch.float32, True),
+             ("exp_avg_sq_scale", exp_avg_sq_scale, torch.float32, True), ("copies", copies, torch.bfloat16, False)]
+    for name, tensors, _, _ in lists:
+        if tensors is not None and len(tensors) != n:
+            raise ValueError(f"{name} must have {n} tensors, got {len(tensors)}")
+    table = _adamw_table(n, lists, decay, dev)
     used = ()
     if stream is not None:
         used = (*params, *grads, *exp_avg, *exp_avg_sq, *(exp_avg_scale or ()), *(exp_avg_sq_scale or ()),

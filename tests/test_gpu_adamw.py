@@ -12,6 +12,7 @@ import pytest
 import torch
 
 import linear_attention_sequence_shortconv_b200 as prism
+from linear_attention_sequence_shortconv_b200 import layer_ops
 from oracle import layer_oracle as ref
 
 pytestmark = pytest.mark.gpu
@@ -258,6 +259,24 @@ def test_another_stream_and_repetition():
         assert all(torch.equal(s, t) for x, y in zip(runs[0], other) for s, t in zip(x, y))
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_both_ways_to_read_the_lists_agree(bits, monkeypatch):
+    p0, g0, _, _ = _inputs(SIZES, "fp32", "bf16")
+    runs = []
+    for slow in (False, True):
+        if slow:
+            monkeypatch.setattr(layer_ops, "_dl_exchange", lambda: None)
+        else:
+            assert layer_ops._dl_exchange() is not None
+        p = torch.nn.ParameterList([torch.nn.Parameter(t) for t in _cuda(p0)])
+        c = tuple(torch.zeros_like(t, dtype=torch.bfloat16) for t in p)
+        state = prism.adamw_state(list(p), bits=bits)
+        with torch.no_grad():
+            prism.adamw_step(p, _cuda(g0), step=1, copies=c, **HYPER, **state)
+        runs.append([*p, *c] + [t.float() for x in state.values() for t in x])
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
 def test_refusals_name_the_argument():
     t = [torch.zeros(600, device="cuda") for _ in range(4)]
     one = [[x] for x in t]
@@ -267,6 +286,10 @@ def test_refusals_name_the_argument():
         prism.adamw_step(one[0], one[1], one[2], [t[3].bfloat16()])
     with pytest.raises(ValueError, match="shapes"):
         prism.adamw_step(one[0], [t[1][:599]], one[2], one[3])
+    with pytest.raises(ValueError, match="cpu"):
+        prism.adamw_step(one[0], [t[1].cpu()], one[2], one[3])
+    with pytest.raises(Exception):
+        prism.adamw_step(one[0], [None], one[2], one[3])
     with pytest.raises(ValueError, match="contiguous"):
         prism.adamw_step([t[0].view(20, 30).t()], [t[1].view(30, 20)], [t[2].view(30, 20)], [t[3].view(30, 20)])
     with pytest.raises(ValueError, match="exp_avg_scale"):

@@ -220,3 +220,55 @@ def test_struct_matches_the_header():
         _fields_ = [(n, ctypes.c_void_p) for n in "pgmvabc"] + [("n", ctypes.c_longlong), ("wd", ctypes.c_double)]
 
     assert ctypes.sizeof(T) == struct.calcsize("@7PQd") == 72
+
+
+class DL(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("device_type", ctypes.c_int32), ("device_id", ctypes.c_int32),
+                ("ndim", ctypes.c_int32), ("code", ctypes.c_uint8), ("bits", ctypes.c_uint8),
+                ("lanes", ctypes.c_uint16), ("shape", ctypes.POINTER(ctypes.c_int64)),
+                ("strides", ctypes.POINTER(ctypes.c_int64)), ("offset", ctypes.c_uint64)]
+
+
+def _dl(shape, strides=None, device=(2, 0), code=2, bits=32, lanes=1, data=0x1000, offset=0):
+    arr = lambda x: (ctypes.c_int64 * max(1, len(x)))(*x)  # noqa: E731
+    return DL(data, *device, len(shape), code, bits, lanes, arr(shape), None if strides is None else arr(strides), offset)
+
+
+def _gather(tensors, like=None, block=0, fail=None):
+    """prism_dl_pointers over described tensors: (returned, pointers, counts)."""
+    L = prism.lib()
+    view = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.POINTER(DL))
+
+    def look(obj, out):
+        i = (obj or 0) - 1
+        if i == fail:
+            return -1
+        ctypes.memmove(out, ctypes.byref(tensors[i]), ctypes.sizeof(DL))
+        return 0
+
+    n = len(tensors)
+    objects, out, views = (ctypes.c_void_p * n)(*range(1, n + 1)), (ctypes.c_uint64 * (9 * n))(), (DL * n)()
+    ref = None if like is None else (DL * n)(*like)
+    fn = L.prism_dl_pointers
+    at = ctypes.addressof(out)
+    got = fn(n, objects, view(look), 0, 2, 32, ref, block, views, ctypes.c_void_p(at), ctypes.c_void_p(at + 56),
+             ctypes.c_size_t(72))
+    return got, list(out[0::9]), list(out[7::9])
+
+
+def test_dl_pointers():
+    assert ctypes.sizeof(DL) == 48
+    ok = [_dl([2, 3], [3, 1]), _dl([], [], data=0x2000), _dl([4, 1, 5], [5, 99, 1], data=0x3000, offset=64), _dl([0, 7], [7, 1]),
+          _dl([6])]
+    assert _gather(ok) == (5, [0x1000, 0x2000, 0x3040, 0x1000, 0x1000], [6, 1, 20, 0, 6])
+    assert _gather(ok, like=ok)[0] == 5
+    bad = [_dl([2, 3], [1, 2]), _dl([2, 3], [4, 1]), _dl([3], [0]), _dl([2], device=(1, 0)), _dl([2], device=(2, 1)),
+           _dl([2], code=4, bits=16), _dl([2], bits=64), _dl([2], lanes=2)]
+    for b in bad:
+        assert _gather([ok[0], ok[4], b])[0] == 2
+    assert _gather(ok, fail=3)[0] == 3
+    # shapes are compared, or the numbers of blocks
+    assert _gather([_dl([6])], like=[_dl([2, 3])])[0] == 0
+    assert _gather([_dl([3, 2])], like=[_dl([2, 3])])[0] == 0
+    assert _gather([_dl([2]), _dl([1]), _dl([0])], like=[_dl([257]), _dl([16, 16]), _dl([0, 3])], block=256)[0] == 3
+    assert _gather([_dl([1])], like=[_dl([257])], block=256)[0] == 0
