@@ -1,0 +1,220 @@
+"""The operators around the mixer together with it, as a model uses them: one training step of
+a one-layer model (embedding, pre-norm, mixer, readout norm, block border; their backward; the
+optimiser), and the same model served token by token.
+
+Both run in fp32 and are held to the error bars of the mixer's own tests: 1e-4 forward, 2e-4
+for gradients, relative to the largest value (the operators around the mixer add a few units
+of 2^-24, far below).
+"""
+import math
+
+import pytest
+import torch
+
+import linear_attention_sequence_shortconv_b200 as prism
+from oracle import layer_oracle as ref
+from oracle.prism_grad import prism_seq_torch
+
+pytestmark = pytest.mark.gpu
+
+B, T, H, d, V, W = 3, 90, 2, 32, 41, 4
+D = H * d
+EPS, SCALE = 1e-5, math.sqrt(D)
+LENGTHS = [90, 0, 33]
+HYPER = dict(lr=1e-2, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1)
+
+
+def _params():
+    g = torch.Generator().manual_seed(1)
+    r = lambda *s, std: std * torch.randn(s, generator=g)  # noqa: E731
+    return {"table": r(V, D, std=0.1), "norm1": 1 + r(D, std=0.1), "wq": r(D, D, std=0.1), "wk": r(D, D, std=0.1),
+            "wv": r(D, D, std=0.1), "wg": r(D, D, std=0.1), "wb": r(D, 2 * H, std=0.1), "conv_w": r(H, d, W, std=0.5),
+            "norm_o": 1 + r(d, std=0.1), "wo": r(D, D, std=0.1), "post": 1 + r(D, std=0.1),
+            "scale": 0.5 + r(D, std=0.1), "norm2": 1 + r(D, std=0.1)}
+
+
+def _batch():
+    g = torch.Generator().manual_seed(2)
+    ids = torch.randint(0, V, (B, T), generator=g)
+    keep = ref.valid_rows(LENGTHS, B, T)[..., None]
+    return ids, torch.randn((B, T, D), generator=g) * keep, torch.randn((B, T, D), generator=g) * keep
+
+
+def _gates(h, wb):
+    s = torch.sigmoid(h @ wb)
+    return (0.5 + 0.5 * s[..., :H]).contiguous(), s[..., H:].contiguous()  # decay, step size
+
+
+def _heads(x):
+    return x.view(*x.shape[:-1], H, d)
+
+
+def _unit(x):
+    """Keys and queries of unit length, as the mixer's callers make them: the state's transition
+    gamma (I - beta k k^T) has the eigenvalue gamma (1 - beta |k|^2), which is stable for
+    beta |k|^2 < 2; the projections here have |k|^2 near 20, and an error would grow by 7 a token."""
+    return x / x.square().sum(-1, keepdim=True).add(1e-12).sqrt()
+
+
+def _unit_grad(x, g):
+    n, u = x.square().sum(-1, keepdim=True).add(1e-12).sqrt(), _unit(x)
+    return (g - u * (u * g).sum(-1, keepdim=True)) / n
+
+
+def _reference(p, ids, dh, dx):
+    """Loss and gradients in fp64 by automatic differentiation."""
+    p = {n: t.double().requires_grad_(True) for n, t in p.items()}
+    x = ref.embed(ids, p["table"], SCALE, LENGTHS)
+    _, h = ref.block_norm(x, p["norm1"], lengths=LENGTHS, eps=EPS)
+    q, k, v, g = (_heads(h @ p[n]) for n in ("wq", "wk", "wv", "wg"))
+    gamma, beta = _gates(h, p["wb"])
+    o, _ = prism_seq_torch(_unit(q), _unit(k), v, gamma, beta, None, None, None, p["conv_w"], lengths=LENGTHS)
+    y = ref.gated_norm(o, g, p["norm_o"], LENGTHS, EPS)
+    x2, h2 = ref.block_norm(x, p["norm2"], y.reshape(B, T, D) @ p["wo"], p["post"], p["scale"], 1.0, LENGTHS, EPS)
+    loss = (h2 * dh.double()).sum() + (x2 * dx.double()).sum()
+    grads = torch.autograd.grad(loss, list(p.values()), allow_unused=True)
+    return h2.detach(), {n: torch.zeros_like(t) if gr is None else gr for (n, t), gr in zip(p.items(), grads)}
+
+
+def _rel(got, want):
+    return ((got.double().cpu() - want).abs().max() / want.abs().max().clamp_min(1e-12)).item()
+
+
+def _forward(p, ids, lens):
+    x = prism.embed_fwd(ids, p["table"], scale=SCALE, lengths=lens)
+    _, h = prism.block_norm_fwd(x, p["norm1"], lengths=lens, eps=EPS)
+    q, k, v = (_heads(h @ p[n]) for n in ("wq", "wk", "wv"))
+    gate = _heads(h @ p["wg"])
+    gamma, beta = _gates(h, p["wb"])
+    o, _ = prism.scan_fwd(_unit(q), _unit(k), v, gamma, beta, None, None, None, p["conv_w"], L=1, chunk=16, lengths=lens)
+    y = prism.gated_norm_fwd(o, gate, p["norm_o"], lengths=lens, eps=EPS)
+    z = y.view(B, T, D) @ p["wo"]
+    x2, h2 = prism.block_norm_fwd(x, p["norm2"], y=z, post_weight=p["post"], scale=p["scale"], lengths=lens, eps=EPS)
+    return x, h, (q, k, v, gamma, beta), gate, o, y, z, x2, h2
+
+
+def _flat(x):
+    return x.reshape(-1, x.shape[-1])
+
+
+@pytest.fixture(autouse=True)
+def full_fp32_products():
+    before = torch.backends.cuda.matmul.allow_tf32
+    torch.backends.cuda.matmul.allow_tf32 = False
+    yield
+    torch.backends.cuda.matmul.allow_tf32 = before
+
+
+def test_training_step():
+    p0 = _params()
+    ids0, dh0, dx0 = _batch()
+    h64, want = _reference(p0, ids0, dh0, dx0)
+    p = {n: t.cuda() for n, t in p0.items()}
+    ids, dh, dx = ids0.cuda(), dh0.cuda(), dx0.cuda()
+    lens = torch.tensor(LENGTHS, dtype=torch.int32).cuda()
+    x, h, (q, k, v, gamma, beta), gate, o, y, z, x2, h2 = _forward(p, ids, lens)
+    assert _rel(h2, h64) <= 1e-4
+
+    g = {}
+    b2 = prism.block_norm_bwd(x2, p["norm2"], dh, y=z, post_weight=p["post"], scale=p["scale"], dx_out=dx,
+                              lengths=lens, eps=EPS)
+    g["norm2"], g["post"], g["scale"] = b2["weight"], b2["post_weight"], b2["scale"]
+    g["wo"] = _flat(y.view(B, T, D)).t() @ _flat(b2["y"])
+    dy = _heads(b2["y"] @ p["wo"].t())
+    gn = prism.gated_norm_bwd(o, gate, p["norm_o"], dy, lengths=lens, eps=EPS)
+    g["norm_o"] = gn["weight"]
+    s = prism.scan_bwd(_unit(q), _unit(k), v, gamma, beta, None, None, None, p["conv_w"], gn["o"], L=1, lengths=lens)
+    g["conv_w"] = s["conv_w"]
+    dh1 = torch.zeros_like(h)
+    for n, t in (("wq", _unit_grad(q, s["q"])), ("wk", _unit_grad(k, s["k"])), ("wv", s["v"]), ("wg", gn["gate"])):
+        t = t.reshape(B, T, D)
+        g[n] = _flat(h).t() @ _flat(t)
+        dh1 += t @ p[n].t()
+    sg, sb = 2 * gamma - 1, beta  # gamma = (1 + sigmoid) / 2
+    db = torch.cat([0.5 * s["gamma"] * sg * (1 - sg), s["beta"] * sb * (1 - sb)], -1)
+    g["wb"] = _flat(h).t() @ _flat(db)
+    dh1 += db @ p["wb"].t()
+    b1 = prism.block_norm_bwd(x, p["norm1"], dh1, dx_out=b2["x"], lengths=lens, eps=EPS)
+    g["norm1"] = b1["weight"]
+    g["table"] = prism.embed_bwd(ids, b1["x"], V, scale=SCALE, lengths=lens)
+    assert prism.stream_status() == 0
+    for n in p:  # conv_w has no gradient where there is no residual write
+        assert (_rel(g[n], want[n]) <= 2e-4) if want[n].any() else not g[n].any(), n
+
+    # the optimiser, on the gradients as they are
+    names = list(p)
+    before = {n: p[n].cpu().double() for n in names}
+    for bits in (32, 8):
+        params = [p0[n].cuda() for n in names]
+        state = prism.adamw_state(params, bits=bits)
+        prism.adamw_step(params, [g[n] for n in names], step=1, **HYPER, **state)
+        for t, n in zip(params, names):
+            zero = torch.zeros_like(before[n])
+            new, _, _ = ref.adamw(before[n], g[n].cpu().double(), zero, zero, 1, HYPER["lr"], HYPER["betas"],
+                                  HYPER["eps"], HYPER["weight_decay"])
+            # the first step moves every parameter by at most lr: 32 roundings of |p| + lr
+            assert ((t.cpu().double() - new).abs() <= 32 * 2.0 ** -24 * (before[n].abs() + 2 * HYPER["lr"])).all(), n
+
+
+def test_serving_token_by_token_is_the_forward():
+    p = {n: t.cuda() for n, t in _params().items()}
+    ids = _batch()[0].cuda()
+    steps = 20
+    *_, h2 = _forward(p, ids, None)
+    S = torch.zeros((B, H, d, d), device="cuda")
+    hist = torch.zeros((B, H, W - 1, d), device="cuda")
+    worst = 0.0
+    for t in range(steps):
+        x = prism.embed_fwd(ids[:, t].contiguous(), p["table"], scale=SCALE)
+        _, h = prism.block_norm_fwd(x, p["norm1"], eps=EPS)
+        q, k, v, gate = (_heads(h @ p[n]) for n in ("wq", "wk", "wv", "wg"))
+        gamma, beta = _gates(h, p["wb"])
+        o = prism.decode_step(_unit(q), _unit(k), v, gamma, beta, None, None, None, p["conv_w"], hist, S, L=1)
+        y = prism.gated_norm_fwd(o, gate, p["norm_o"], eps=EPS)
+        _, out = prism.block_norm_fwd(x, p["norm2"], y=y.view(B, D) @ p["wo"], post_weight=p["post"],
+                                      scale=p["scale"], eps=EPS)
+        worst = max(worst, ((out - h2[:, t]).abs().max() / h2.abs().max()).item())
+    assert prism.stream_status() == 0 and worst <= 1e-4
+
+
+def test_training_step_replayed_from_a_graph():
+    # forward, backward of the operators and the optimiser in one captured graph, with the step
+    # and the rate on the device: as the same calls made one by one
+    p0 = _params()
+    ids0, dh0, dx0 = _batch()
+    lens = torch.tensor(LENGTHS, dtype=torch.int32).cuda()
+    dh, dx = dh0.cuda(), dx0.cuda()
+    names = ["table", "norm1", "post", "scale", "norm2"]
+    runs = []
+    for captured in (False, True):
+        p = {n: p0[n].cuda() for n in names}
+        state = prism.adamw_state([p[n] for n in names], bits=8)
+        ids = ids0.cuda()
+        step, lr = torch.ones(1, dtype=torch.int32, device="cuda"), torch.full((1,), 1e-2, device="cuda")
+
+        def one():
+            x = prism.embed_fwd(ids, p["table"], scale=SCALE, lengths=lens)
+            _, z = prism.block_norm_fwd(x, p["norm1"], lengths=lens)
+            x2, _ = prism.block_norm_fwd(x, p["norm2"], y=z, post_weight=p["post"], scale=p["scale"], lengths=lens)
+            b2 = prism.block_norm_bwd(x2, p["norm2"], dh, y=z, post_weight=p["post"], scale=p["scale"], dx_out=dx,
+                                      lengths=lens)
+            b1 = prism.block_norm_bwd(x, p["norm1"], b2["y"], dx_out=b2["x"], lengths=lens)
+            dt = prism.embed_bwd(ids, b1["x"], V, scale=SCALE, lengths=lens)
+            prism.adamw_step([p[n] for n in names],
+                             [dt, b1["weight"], b2["post_weight"], b2["scale"], b2["weight"]],
+                             **dict(HYPER, step=step, lr=lr), **state)
+
+        graph = None
+        if captured:
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                one()
+        for i in range(4):
+            step.fill_(i + 1)
+            ids.copy_(torch.roll(ids0, i, 1))
+            graph.replay() if captured else one()
+        torch.cuda.synchronize()
+        runs.append([p[n] for n in names] + [t.float() for x in state.values() for t in x])
+    assert prism.stream_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
