@@ -41,7 +41,7 @@ __device__ __forceinline__ uint32_t token_key(const EmbedParams& p, long long n)
 // A block takes `tile` tokens: their keys go to shared memory, then its threads walk the rows'
 // 16-byte (eight-element) pieces one after the other, so that no lane idles at any width.
 template <typename I, typename W, typename T, bool VEC>
-__global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(EmbedParams p, int tile, int pieces) {
+__global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(EmbedParams p, int tile, FastDiv pieces) {
   __shared__ uint32_t key[kEmbedFwdTile];
   const long long first = (long long)blockIdx.x * tile;
   const int rows = (int)(p.N - first < tile ? p.N - first : tile);
@@ -49,10 +49,10 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(EmbedParams p, i
   __syncthreads();
   const W* table = static_cast<const W*>(p.table);
   T* out = static_cast<T*>(p.out) + first * p.D;
-  const int n = rows * pieces;
+  const int n = rows * (int)pieces.d;
 #pragma unroll 4
   for (int i = threadIdx.x; i < n; i += kFwdThreads) {
-    const int r = (int)((uint32_t)i / (uint32_t)pieces), c = i - r * pieces;
+    const int r = (int)pieces.div32((uint32_t)i), c = i - r * (int)pieces.d;
     const bool ok = key[r] < (uint32_t)p.V;
     if (VEC) {
       float x[8];
@@ -365,7 +365,8 @@ __device__ __forceinline__ const uint2* sorted_pairs(const EmbedParams& p, const
 // tpr.  blockIdx.y is the tile of 8 tpr columns.
 constexpr int kSumThreads = 256;
 constexpr int kZeroRows = 64;  // table rows that one zeroing block looks after
-constexpr int kLongChunks = 32;
+constexpr int kJoinThreads = 512;
+constexpr int kLongChunks = 8;   // chunks whose long runs one block takes
 constexpr int kShortRun = 8;   // partial sums behind a run's first up to which one thread group joins it
 
 // Eight columns as they lie in memory.
@@ -410,15 +411,27 @@ struct Columns {
         if (first + e * step < D) row[first + e * step] = x[e];
     }
   }
-  // the finished sum of table row v
+  // The finished sum of table row v.  Adding to what the row holds takes the memory's own add, so
+  // that nobody waits for the old values; each element gets one addition in all (a row is finished
+  // once), so the order of execution does not show.  That add treats subnormal numbers as zero.
   __device__ __forceinline__ void finish(const EmbedParams& p, uint32_t v, const float (&x)[8]) const {
     float* row = p.d_table + (size_t)v * D;
     float y[8];
-    if (p.accumulate) load(row, y);
-    else zero8(y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] += p.scale * x[e];
-    store(row, y);
+    for (int e = 0; e < 8; ++e) y[e] = p.scale * x[e];
+    if (!p.accumulate) return store(row, y);
+    if (VEC) {
+      if (first >= D) return;
+#pragma unroll
+      for (int e = 0; e < 8; e += 4)
+        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(row + first + e), "f"(y[e]), "f"(y[e + 1]),
+                     "f"(y[e + 2]), "f"(y[e + 3]) : "memory");
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (first + e * step < D)
+          asm volatile("red.global.add.f32 [%0], %1;" ::"l"(row + first + e * step), "f"(y[e]) : "memory");
+    }
   }
 };
 
@@ -466,7 +479,7 @@ __device__ __forceinline__ void zero_absent_rows(const EmbedParams& p, const uin
 // Blocks below `zero_blocks` look after the rows without a token; a thread group of the others
 // walks the runs of one chunk, eight columns per thread (blockIdx.y: tile of 8 tpr columns).
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(EmbedParams p, EmbedPlan plan, int tpr, int groups,
+__global__ void __launch_bounds__(kSumThreads, 3) embed_sum_kernel(EmbedParams p, EmbedPlan plan, int tpr, int groups,
                                                                    int zero_blocks) {
   extern __shared__ uint2 staged_pairs[];  // of the block's positions
   const uint2* pairs = sorted_pairs(p, plan);
@@ -542,11 +555,14 @@ struct Runs {
   int chunk, chunks;
   // key at the first position of chunk n (`none` behind the last)
   __device__ __forceinline__ uint32_t at(long long n) const { return n < chunks ? pairs[n * chunk].x : none; }
-  // the id of the run that begins in chunk c and goes on behind it, or `none`
-  __device__ __forceinline__ uint32_t begins(long long c) const {
-    if (c + 1 >= chunks) return none;
-    const uint32_t next = at(c + 1), last = pairs[(c + 1) * chunk - 1].x, prior = c ? pairs[c * chunk - 1].x : none;
-    return next == last && prior != last ? last : none;
+  // the id of the run that begins in chunk c and goes on behind it, or `none`; `far`: the key at
+  // the first position of chunk c + 1 + kShortRun.  The loads do not wait for one another.
+  __device__ __forceinline__ uint32_t begins(long long c, uint32_t* far) const {
+    const bool in = c + 1 < chunks;
+    const uint32_t next = at(c + 1), last = in ? pairs[(c + 1) * chunk - 1].x : none;
+    const uint32_t prior = in && c ? pairs[c * chunk - 1].x : none;
+    *far = at(c + 1 + kShortRun);
+    return in && next == last && prior != last ? last : none;
   }
 };
 
@@ -556,24 +572,26 @@ struct Runs {
 // longer runs that begin there: the block's groups add equal slices of the partial sums, whose
 // sums are then added from left to right.
 template <bool VEC>
-__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(EmbedParams p, EmbedPlan plan, int width,
+__global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(EmbedParams p, EmbedPlan plan, int width,
                                                                  int short_blocks) {
-  __shared__ uint32_t found;
-  __shared__ __align__(16) float slice[kSumThreads * 8];  // written in 16-byte pieces
+  __shared__ uint32_t found, ids[kLongChunks];
+  __shared__ __align__(16) float slice[kJoinThreads * 8];  // written in 16-byte pieces
   const Runs runs{sorted_pairs(p, plan), (uint32_t)p.V, plan.chunk, plan.chunks};
-  const int groups = kSumThreads / width, group = threadIdx.x / width, gt = threadIdx.x - group * width;
+  const int groups = kJoinThreads / width, group = threadIdx.x / width, gt = threadIdx.x - group * width;
   const Columns<VEC> col(gt, width, blockIdx.y, p.D);
   float acc[8], x[8];
   wait_for_previous();
   if ((int)blockIdx.x < short_blocks) {
     if (group >= groups) return;
     const long long c = (long long)blockIdx.x * groups + group;
-    const uint32_t id = runs.begins(c);
-    if (id == runs.none) return;
+    uint32_t far, key[kShortRun];
+#pragma unroll
+    for (int n = 0; n < kShortRun; ++n) key[n] = runs.at(c + 1 + n);
+    const uint32_t id = runs.begins(c, &far);
+    if (id == runs.none || far == id) return;
     int heads = 0;
 #pragma unroll
-    for (int n = 1; n <= kShortRun + 1; ++n) heads += runs.at(c + n) == id;
-    if (heads > kShortRun) return;
+    for (int n = 0; n < kShortRun; ++n) heads += key[n] == id;
     col.load(p.part + ((size_t)c * 2 + 1) * p.D, acc);
 #pragma unroll 4
     for (int n = 1; n <= heads; ++n) {
@@ -584,25 +602,28 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(EmbedParams p, 
     col.finish(p, id, acc);
     return;
   }
+  const int slices = groups < 32 ? groups : 32;
   const long long c0 = (long long)(blockIdx.x - short_blocks) * kLongChunks;
-  if (threadIdx.x < kLongChunks) {
-    const uint32_t own = runs.begins(c0 + threadIdx.x);
-    const uint32_t far = __ballot_sync(0xffffffffu, own != runs.none && runs.at(c0 + threadIdx.x + kShortRun + 1) == own);
-    if (threadIdx.x == 0) found = far;
+  if (threadIdx.x < 32) {
+    uint32_t far = runs.none;
+    const uint32_t own = threadIdx.x < kLongChunks ? runs.begins(c0 + threadIdx.x, &far) : runs.none;
+    const uint32_t some = __ballot_sync(0xffffffffu, own != runs.none && far == own);
+    if (threadIdx.x == 0) found = some;
+    if (threadIdx.x < kLongChunks) ids[threadIdx.x] = own;
   }
   __syncthreads();
   for (uint32_t left = found; left; left &= left - 1) {
     const long long c = c0 + __ffs(left) - 1;
-    const uint32_t id = runs.at(c + 1);
+    const uint32_t id = ids[__ffs(left) - 1];
     long long heads = 0;  // chunks behind c that the run reaches: a prefix, since the keys are sorted
     for (;;) {
       const int got = __syncthreads_count(runs.at(c + 1 + heads + threadIdx.x) == id);
       heads += got;
-      if (got < kSumThreads) break;
+      if (got < kJoinThreads) break;
     }
     zero8(acc);
-    if (group < groups) {
-      const long long lo = heads * group / groups, hi = heads * (group + 1) / groups;
+    if (group < slices) {
+      const long long lo = heads * group / slices, hi = heads * (group + 1) / slices;
       if (group == 0) col.load(p.part + ((size_t)c * 2 + 1) * p.D, acc);
 #pragma unroll 8
       for (long long n = lo; n < hi; ++n) {
@@ -614,7 +635,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(EmbedParams p, 
     store8(slice + 8 * threadIdx.x, acc);
     __syncthreads();
     if (group == 0) {
-      for (int g = 1; g < groups; ++g) {
+      for (int g = 1; g < slices; ++g) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) acc[q] += slice[8 * (g * width + gt) + q];
       }
@@ -633,9 +654,9 @@ cudaError_t embed_fwd_types(const EmbedParams& p, cudaStream_t stream) {
   tile = tile < 1 ? 1 : tile > kEmbedFwdTile ? kEmbedFwdTile : tile;
   const int blocks = (int)((p.N + tile - 1) / tile);
   if (vec)
-    embed_fwd_kernel<I, W, T, true><<<blocks, kFwdThreads, 0, stream>>>(p, tile, pieces);
+    embed_fwd_kernel<I, W, T, true><<<blocks, kFwdThreads, 0, stream>>>(p, tile, FastDiv(pieces));
   else
-    embed_fwd_kernel<I, W, T, false><<<blocks, kFwdThreads, 0, stream>>>(p, tile, pieces);
+    embed_fwd_kernel<I, W, T, false><<<blocks, kFwdThreads, 0, stream>>>(p, tile, FastDiv(pieces));
   return cudaGetLastError();
 }
 
@@ -700,11 +721,11 @@ cudaError_t embed_sums(const EmbedParams& p, const EmbedPlan& plan, cudaStream_t
   cudaError_t err = launch_chained(embed_sum_kernel<T, VEC>, dim3(sum_blocks + zero_blocks, tiles), threads,
                                    (size_t)groups * plan.chunk * 8, stream, p, plan, tpr, groups, zero_blocks);
   if (err != cudaSuccess || plan.chunks == 1) return err;
-  const int width = need < 32 ? need : 32, joins = kSumThreads / width;
+  const int width = need < 32 ? need : 32, joins = kJoinThreads / width;
   const int short_blocks = (plan.chunks + joins - 1) / joins;
   const int long_blocks = plan.chunks > kShortRun + 1 ? (plan.chunks + kLongChunks - 1) / kLongChunks : 0;
   return launch_chained(embed_join_kernel<VEC>, dim3(short_blocks + long_blocks, (need + width - 1) / width),
-                        kSumThreads, 0, stream, p, plan, width, short_blocks);
+                        kJoinThreads, 0, stream, p, plan, width, short_blocks);
 }
 
 }  // namespace
