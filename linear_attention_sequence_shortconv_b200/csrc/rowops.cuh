@@ -217,13 +217,15 @@ struct FastDiv {
   __device__ __forceinline__ long long div(long long n) const {
     return n >> 32 ? n / d : (long long)div32((uint32_t)n);
   }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return div32(n); }
 };
 
 // Whether token n = b T + t of a right-padded batch is a valid step (t < lengths[b]).
-__device__ __forceinline__ bool token_valid(long long n, const FastDiv& T, const int32_t* lengths) {
+template <typename Index>
+__device__ __forceinline__ bool token_valid(Index n, const FastDiv& T, const int32_t* lengths) {
   if (!lengths) return true;
-  const long long b = T.div(n);
-  return n - b * T.d < __ldg(lengths + b);
+  const Index b = T.div(n);
+  return (long long)(n - b * T.d) < __ldg(lengths + b);
 }
 
 // Programmatic launch of the next kernel of a chain: it may start once every block of this one

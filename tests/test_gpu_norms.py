@@ -157,6 +157,17 @@ def test_a_nan_stays_in_its_row():
     assert torch.equal(y, y2)
 
 
+def test_gate_offsets_beyond_32_bits():
+    # three tokens whose gates stand 2^30 elements apart
+    o, g, w, dy = (t.cuda() for t in _gated_inputs(1, 3, 2, 64, torch.bfloat16, "dense"))
+    wide = torch.empty(2 * (1 << 30) + 128, dtype=torch.bfloat16, device="cuda")
+    far = wide.as_strided((1, 3, 2, 64), (3 << 30, 1 << 30, 64, 1))
+    far.copy_(g)
+    assert torch.equal(prism.gated_norm_fwd(o, far, w), prism.gated_norm_fwd(o, g, w))
+    a, b = prism.gated_norm_bwd(o, far, w, dy), prism.gated_norm_bwd(o, g, w, dy)
+    assert all(torch.equal(a[n], b[n]) for n in a)
+
+
 def test_zero_rows():
     o = torch.zeros(2, 3, 2, 64, device="cuda")
     w, dy = torch.ones(64, device="cuda"), torch.ones(2, 3, 2, 64, device="cuda")
