@@ -516,18 +516,27 @@ typedef struct prism_dl_tensor {
 /* DLPack's exchange function of a framework: views `object` as a tensor; 0 on success. */
 typedef int (*prism_dl_from_object)(void* object, prism_dl_tensor* out);
 
+/* What the tensors of one field are: type_code 0 leaves the field out. */
+typedef struct prism_dl_field {
+  int type_code;
+  int type_bits;
+  int block; /* 0: the shapes of the first field; else as many elements as those have blocks of `block` */
+} prism_dl_field;
+
 /*
- * prism_dl_pointers - the data pointers of n objects of a framework, for the host arrays of
- * prism_adamw_step (host only, no CUDA call; a binding's loop over hundreds of tensors).
- * views[i] is what from_object says of objects[i].  The object has to be a dense tensor of the
- * type on CUDA device `device`; with `like`, of like[i]'s shape (block 0) or of as many
- * elements as like[i] has blocks of `block`.  Its pointer goes to out + i * stride, its number
- * of elements (a long long) to count + i * stride where count is given.
- * Returns n, or the index of the first object that is not as described.
+ * prism_dl_pointers - the data pointers of a framework's tensors for a host array of structs,
+ * such as prism_adamw_step's (host only, no CUDA call; a binding's loop over hundreds of
+ * tensors).  objects holds n tensors for each of the `fields` fields that is not left out, one
+ * field after the other; from_object views each.  Every object has to be a dense tensor of its
+ * field's type on CUDA device `device`, and (behind the first field) to match the first field's
+ * tensor of the same place.  The pointer of field f, place i goes to out + i * stride + 8 f, the
+ * first field's numbers of elements (long long) to out + i * stride + count_offset.
+ * views: room for n prism_dl_tensor.  Returns -1, or the index in objects of the first object
+ * that is not as described.
  */
-int prism_dl_pointers(int n, void* const* objects, prism_dl_from_object from_object, int device, int type_code,
-                      int type_bits, const prism_dl_tensor* like, int block, prism_dl_tensor* views, void* out,
-                      void* count, size_t stride);
+int prism_dl_pointers(int fields, const prism_dl_field* spec, int n, void* const* objects,
+                      prism_dl_from_object from_object, int device, prism_dl_tensor* views, void* out, size_t stride,
+                      size_t count_offset);
 
 /* Synchronises `stream`, then returns and clears the device status word of the
  * current device: PRISM_OK, PRISM_ERR_TIMEOUT, PRISM_ERR_BOUNDS, or

@@ -378,35 +378,41 @@ int prism_adamw_step(const prism_adamw_tensor* tensors, int count, int step, con
   return rc;
 }
 
-int prism_dl_pointers(int n, void* const* objects, prism_dl_from_object from_object, int device, int type_code,
-                      int type_bits, const prism_dl_tensor* like, int block, prism_dl_tensor* views, void* out,
-                      void* count, size_t stride) {
-  for (int i = 0; i < n; ++i) {
-    prism_dl_tensor& v = views[i];
-    if (from_object(objects[i], &v) != 0) return i;
-    if (v.device_type != 2 || v.device_id != device || v.type_code != type_code || v.type_bits != type_bits ||
-        v.type_lanes != 1)
-      return i;
-    long long elements = 1;
-    for (int d = 0; d < v.ndim; ++d) elements *= v.shape[d];
-    long long step = 1;  // dense, as far as it matters: the stride of a dimension of one element does not
-    for (int d = v.ndim - 1; d >= 0 && v.strides && elements > 0; --d) {
-      if (v.shape[d] != 1 && v.strides[d] != step) return i;
-      step *= v.shape[d];
+int prism_dl_pointers(int fields, const prism_dl_field* spec, int n, void* const* objects,
+                      prism_dl_from_object from_object, int device, prism_dl_tensor* views, void* out, size_t stride,
+                      size_t count_offset) {
+  int at = 0;
+  for (int f = 0; f < fields; ++f) {
+    if (spec[f].type_code == 0) continue;
+    for (int i = 0; i < n; ++i, ++at) {
+      prism_dl_tensor other;
+      prism_dl_tensor& v = f == 0 ? views[i] : other;
+      if (from_object(objects[at], &v) != 0) return at;
+      if (v.device_type != 2 || v.device_id != device || v.type_code != spec[f].type_code ||
+          v.type_bits != spec[f].type_bits || v.type_lanes != 1)
+        return at;
+      long long elements = 1;
+      for (int d = 0; d < v.ndim; ++d) elements *= v.shape[d];
+      long long step = 1;  // dense, as far as it matters: the stride of a dimension of one element does not
+      for (int d = v.ndim - 1; d >= 0 && v.strides && elements > 0; --d) {
+        if (v.shape[d] != 1 && v.strides[d] != step) return at;
+        step *= v.shape[d];
+      }
+      char* row = static_cast<char*>(out) + i * stride;
+      if (f == 0) {
+        *reinterpret_cast<long long*>(row + count_offset) = elements;
+      } else if (spec[f].block > 0) {
+        const long long of = *reinterpret_cast<const long long*>(row + count_offset);
+        if (elements != (of + spec[f].block - 1) / spec[f].block) return at;
+      } else {
+        if (v.ndim != views[i].ndim) return at;
+        for (int d = 0; d < v.ndim; ++d)
+          if (v.shape[d] != views[i].shape[d]) return at;
+      }
+      *reinterpret_cast<void**>(row + 8 * f) = static_cast<char*>(v.data) + v.byte_offset;
     }
-    if (like && block > 0) {
-      long long of = 1;
-      for (int d = 0; d < like[i].ndim; ++d) of *= like[i].shape[d];
-      if (elements != (of + block - 1) / block) return i;
-    } else if (like) {
-      if (v.ndim != like[i].ndim) return i;
-      for (int d = 0; d < v.ndim; ++d)
-        if (v.shape[d] != like[i].shape[d]) return i;
-    }
-    *reinterpret_cast<void**>(static_cast<char*>(out) + i * stride) = static_cast<char*>(v.data) + v.byte_offset;
-    if (count) *reinterpret_cast<long long*>(static_cast<char*>(count) + i * stride) = elements;
   }
-  return n;
+  return -1;
 }
 
 }  // extern "C"

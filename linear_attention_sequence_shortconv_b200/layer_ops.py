@@ -11,6 +11,7 @@ import array
 import contextlib
 import ctypes
 import functools
+import itertools
 from typing import Dict, List, Optional, Sequence, Union
 
 import torch
@@ -367,7 +368,7 @@ def _dl_exchange():
     gather = ctypes.PyDLL(LIB_PATH).prism_dl_pointers
     vp, ci = ctypes.c_void_p, ctypes.c_int
     gather.restype = ci
-    gather.argtypes = [ci, vp, vp, ci, ci, ci, vp, ci, vp, vp, vp, ctypes.c_size_t]
+    gather.argtypes = [ci, vp, ci, vp, vp, ci, vp, vp, ctypes.c_size_t, ctypes.c_size_t]
     return gather, view
 
 
@@ -375,22 +376,18 @@ def _adamw_table(n, lists, decay, dev):
     """The host array of prism_adamw_tensor of a step, its tensors checked."""
     table = ctypes.create_string_buffer(_ADAMW_TENSOR * n)
     memoryview(table).cast("B").cast("d")[8::9] = memoryview(decay)
-    at = ctypes.addressof(table)
     exchange = _dl_exchange()
     if exchange is not None:
         gather, view = exchange
-        first, views = ctypes.create_string_buffer(_DL_TENSOR * n), ctypes.create_string_buffer(_DL_TENSOR * n)
-        objects = ctypes.c_void_p * n
-        for field, (_, tensors, dtype, blocks) in enumerate(lists):
-            if tensors is None:
-                continue
-            code, bits = _DL_TYPES[dtype]
-            if gather(n, objects(*map(id, tensors)), view, dev.index, code, bits, None if field == 0 else first,
-                      STATE_BLOCK if blocks else 0, first if field == 0 else views, at + 8 * field,
-                      at + 56 if field == 0 else None, _ADAMW_TENSOR) != n:
-                break  # the checks below say which and why
-        else:
+        given = [tensors for _, tensors, _, _ in lists if tensors is not None]
+        spec = array.array("i", [x for _, tensors, dtype, blocks in lists
+                                 for x in (*(_DL_TYPES[dtype] if tensors is not None else (0, 0)),
+                                           STATE_BLOCK if blocks else 0)])
+        objects = array.array("Q", map(id, itertools.chain.from_iterable(given)))
+        if gather(len(lists), spec.buffer_info()[0], n, objects.buffer_info()[0], view, dev.index,
+                  ctypes.create_string_buffer(_DL_TENSOR * n), table, _ADAMW_TENSOR, 56) < 0:
             return table
+        # the checks below say what is wrong with which
     fields = memoryview(table).cast("B").cast("Q")
     params = lists[0][1]
     for field, (name, tensors, dtype, blocks) in enumerate(lists):

@@ -234,41 +234,42 @@ def _dl(shape, strides=None, device=(2, 0), code=2, bits=32, lanes=1, data=0x100
     return DL(data, *device, len(shape), code, bits, lanes, arr(shape), None if strides is None else arr(strides), offset)
 
 
-def _gather(tensors, like=None, block=0, fail=None):
-    """prism_dl_pointers over described tensors: (returned, pointers, counts)."""
-    L = prism.lib()
+def _gather(*fields, block=0, code=2, bits=32, fail=None, skip=()):
+    """prism_dl_pointers over described tensors: (returned, pointers per field, counts)."""
+    flat = [t for f, ts in enumerate(fields) if f not in skip for t in ts]
     view = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.POINTER(DL))
 
     def look(obj, out):
         i = (obj or 0) - 1
         if i == fail:
             return -1
-        ctypes.memmove(out, ctypes.byref(tensors[i]), ctypes.sizeof(DL))
+        ctypes.memmove(out, ctypes.byref(flat[i]), ctypes.sizeof(DL))
         return 0
 
-    n = len(tensors)
-    objects, out, views = (ctypes.c_void_p * n)(*range(1, n + 1)), (ctypes.c_uint64 * (9 * n))(), (DL * n)()
-    ref = None if like is None else (DL * n)(*like)
-    fn = L.prism_dl_pointers
-    at = ctypes.addressof(out)
-    got = fn(n, objects, view(look), 0, 2, 32, ref, block, views, ctypes.c_void_p(at), ctypes.c_void_p(at + 56),
-             ctypes.c_size_t(72))
-    return got, list(out[0::9]), list(out[7::9])
+    n = len(fields[0])
+    spec = [x for f in range(len(fields)) for x in ((0, 0, 0) if f in skip else (code, bits, block if f else 0))]
+    out = (ctypes.c_uint64 * (9 * n))()
+    got = prism.lib().prism_dl_pointers(
+        len(fields), (ctypes.c_int * len(spec))(*spec), n, (ctypes.c_void_p * len(flat))(*range(1, len(flat) + 1)),
+        view(look), 0, (DL * n)(), out, ctypes.c_size_t(72), ctypes.c_size_t(56))
+    return got, [list(out[f::9]) for f in range(len(fields))], list(out[7::9])
 
 
 def test_dl_pointers():
     assert ctypes.sizeof(DL) == 48
-    ok = [_dl([2, 3], [3, 1]), _dl([], [], data=0x2000), _dl([4, 1, 5], [5, 99, 1], data=0x3000, offset=64), _dl([0, 7], [7, 1]),
-          _dl([6])]
-    assert _gather(ok) == (5, [0x1000, 0x2000, 0x3040, 0x1000, 0x1000], [6, 1, 20, 0, 6])
-    assert _gather(ok, like=ok)[0] == 5
+    ok = [_dl([2, 3], [3, 1]), _dl([], [], data=0x2000), _dl([4, 1, 5], [5, 99, 1], data=0x3000, offset=64),
+          _dl([0, 7], [7, 1]), _dl([6])]
+    where = [0x1000, 0x2000, 0x3040, 0x1000, 0x1000]
+    assert _gather(ok) == (-1, [where], [6, 1, 20, 0, 6])
+    assert _gather(ok, ok, ok, skip=(1,)) == (-1, [where, [0] * 5, where], [6, 1, 20, 0, 6])
     bad = [_dl([2, 3], [1, 2]), _dl([2, 3], [4, 1]), _dl([3], [0]), _dl([2], device=(1, 0)), _dl([2], device=(2, 1)),
            _dl([2], code=4, bits=16), _dl([2], bits=64), _dl([2], lanes=2)]
     for b in bad:
         assert _gather([ok[0], ok[4], b])[0] == 2
-    assert _gather(ok, fail=3)[0] == 3
+    assert _gather(ok, fail=3)[0] == 3 and _gather(ok, ok, fail=7)[0] == 7
     # shapes are compared, or the numbers of blocks
-    assert _gather([_dl([6])], like=[_dl([2, 3])])[0] == 0
-    assert _gather([_dl([3, 2])], like=[_dl([2, 3])])[0] == 0
-    assert _gather([_dl([2]), _dl([1]), _dl([0])], like=[_dl([257]), _dl([16, 16]), _dl([0, 3])], block=256)[0] == 3
-    assert _gather([_dl([1])], like=[_dl([257])], block=256)[0] == 0
+    assert _gather([_dl([2, 3])], [_dl([6])])[0] == 1
+    assert _gather([_dl([2, 3])], [_dl([3, 2])])[0] == 1
+    many = [_dl([257]), _dl([16, 16]), _dl([0, 3])]
+    assert _gather(many, [_dl([2]), _dl([1]), _dl([0])], block=256)[0] == -1
+    assert _gather(many, [_dl([1]), _dl([1]), _dl([0])], block=256)[0] == 3
