@@ -37,8 +37,12 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _check(t, name, dtype=None, required=True, shape=None, device=None):
     """The mixer's check of one tensor argument, with a short way for a tensor that is fine."""
-    if (t is not None and t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype == dtype)
-            and (shape is None or t.shape == shape) and (device is None or t.device == device)):
+    if t is None:
+        if required:
+            raise ValueError(f"{name} is required")
+        return
+    if (t.is_cuda and (dtype is None or t.dtype == dtype) and (shape is None or t.shape == shape)
+            and (device is None or t.get_device() == device.index) and t.is_contiguous()):
         return
     _check_slow(t, name, dtype, required, shape, device)
 
@@ -90,7 +94,7 @@ def _gate_stride(gate, o, sizes) -> int:
     B, T, H, d = sizes
     if gate is None:
         return H * d
-    if gate.shape == o.shape and gate.dtype == o.dtype and gate.device == o.device and gate.is_contiguous():
+    if gate.dtype == o.dtype and gate.shape == o.shape and gate.get_device() == o.get_device() and gate.is_contiguous():
         return H * d
     if not gate.is_cuda or gate.device != o.device:
         raise ValueError(f"gate is on {gate.device}, but the call's tensors are on {o.device}")
