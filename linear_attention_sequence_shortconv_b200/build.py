@@ -7,6 +7,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,7 +20,7 @@ LIB_DEBUG = os.path.join(PKG, "libprism_debug.so")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "--expt-relaxed-constexpr",
 ]
 
@@ -42,26 +44,33 @@ def needs_rebuild(lib: str = LIB) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _command(lib: str, debug: bool) -> list[str]:
-    flags = NVCC_FLAGS + (["-DPRISM_DEBUG_BOUNDS"] if debug else [])
-    return [nvcc(), *flags, "-I", INCLUDE, "-I", CSRC, *sources(), "-o", lib + ".tmp"]
+def _run(cmd: list[str], verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile both libraries (side by side) when a source is newer; returns the release
-    library's path."""
+    """Compile both libraries (all sources side by side) when a source is newer; returns the
+    release library's path."""
     todo = [(lib, debug) for lib, debug in ((LIB, False), (LIB_DEBUG, True)) if force or needs_rebuild(lib)]
-    procs = []
-    for lib, debug in todo:
-        cmd = _command(lib, debug)
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        procs.append((lib, cmd, subprocess.Popen(cmd)))
-    failed = [cmd for _, cmd, proc in procs if proc.wait() != 0]
-    if failed:
-        raise subprocess.CalledProcessError(1, failed[0])
-    for lib, _, _ in procs:
-        os.replace(lib + ".tmp", lib)
+    if not todo:
+        return LIB
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+        objects, jobs = {}, []
+        # the largest sources first, so that none of them is left for the end
+        for src in sorted(sources(), key=os.path.getsize, reverse=True):
+            for lib, debug in todo:
+                obj = os.path.join(tmp, f"{os.path.basename(src)}.{'debug' if debug else 'release'}.o")
+                objects.setdefault(lib, []).append(obj)
+                cmd = [nvcc(), *NVCC_FLAGS, *(["-DPRISM_DEBUG_BOUNDS"] if debug else []), "-I", INCLUDE, "-I", CSRC,
+                       "-c", src, "-o", obj]
+                jobs.append(pool.submit(_run, cmd, verbose))
+        for job in jobs:
+            job.result()
+        for lib, _ in todo:
+            _run([nvcc(), *NVCC_FLAGS, "-shared", *sorted(objects[lib]), "-o", lib + ".tmp"], verbose)
+            os.replace(lib + ".tmp", lib)
     return LIB
 
 

@@ -15,8 +15,13 @@
 // does not depend on any order of execution.  Rows without a token are written as zero by
 // further blocks of the summing launch, so a dense gradient is written exactly once.
 //
-// Bound by memory: d_out is read once and the table's gradient is written once; the pairs are
-// 8 bytes a token and pass.
+// The lookup is bound by memory (recommendation batch, 128 x 1024 ragged tokens, a table of
+// 1000003 x 128 in fp32: 12 us, 4.1 TB/s).  The gradient reads d_out once and writes the table's
+// gradient once, but about half of its time is a chain of steps that each wait for the one
+// before: with rows of 8 elements, where there is nothing to move, 32768 tokens take 33 us (sort
+// 13.5, sums 14, joins 8, less what the chained launches overlap).  Measured: 130M LM, 32768
+// tokens, dense gradient of 32000 x 768: 55 us (floor 22.7); recommendation batch, added to
+// 1000003 x 128: 48 us (floor 11).
 #include <cooperative_groups.h>
 
 #include "embed.cuh"
@@ -151,6 +156,9 @@ __device__ __forceinline__ int block_exclusive_scan(int x, int warps, int* warp_
 // distributed shared memory, orders the pairs by digit in its shared memory and writes them
 // out from there, so that the pairs of a digit leave in runs.  The cluster's barrier orders a
 // pass's pairs before the next one's reads.
+//
+// Against tiles over all SMs: 32768 tokens 14.5 us here and 26 us by tiles; 131072 tokens 41 us
+// (eight pairs a thread, bound by the instructions of 16 SMs) and 26 us.
 constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
 
 template <typename I, int KPT>
