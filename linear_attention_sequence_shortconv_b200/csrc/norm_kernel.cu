@@ -737,11 +737,13 @@ __global__ void __launch_bounds__(kSumCols * kSumSlices) column_sum_kernel(Colum
   }
 }
 
+constexpr size_t kMostSmem = 216 * 1024;  // dynamic shared memory of a block, beside up to 11 KB of static
+
 template <typename... Args>
 cudaError_t launch_with_smem(void (*kernel)(Args...), int blocks, int threads, size_t smem, cudaStream_t stream,
                              Args... args) {
-  if (smem > 32 * 1024) {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 32 * 1024) {  // always the same limit: another thread may be about to launch this kernel
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
     if (err != cudaSuccess) return err;
   }
   kernel<<<blocks, threads, smem, stream>>>(args...);
@@ -796,13 +798,12 @@ cudaError_t gated_bwd_lanes(const GatedNormParams& p, int gate, int blocks, cuda
 // Widths that are not a multiple of 8, or whose rings would not fit the shared memory, take
 // one column per access.
 struct BlockShape {
-  static constexpr size_t kSmem = 220 * 1024;
   int E, tpr, groups;
   bool vec;
   BlockShape(int D, bool bwd, int x_bytes, int bytes) {
     const int arrays = (bwd ? 2 : 1) * (x_bytes + bytes);  // bytes of a column that the ring holds per row
     const size_t row = (size_t)((D + 1023) / 1024 * 1024) * (kBnStages * arrays);
-    vec = D % 8 == 0 && row + (size_t)(D + 1023) / 1024 * 1024 * 12 <= kSmem;
+    vec = D % 8 == 0 && row + (size_t)(D + 1023) / 1024 * 1024 * 12 <= kMostSmem;
     if (bwd) E = D <= 1024 && vec ? (D + 255) / 256 * 8 : vec ? 32 : D <= 4096 ? 8 : 16;
     else E = D <= 1024 ? (D + 255) / 256 * 8 : 16;
     const int t = (D + E - 1) / E, most = bwd ? bwd_threads(E, vec) : fwd_threads(E);
@@ -813,9 +814,10 @@ struct BlockShape {
     if (tpr > 32 && groups > kBnGroups) groups = kBnGroups;
     if (vec) {  // a group's part of the rings and of the backward's column sums
       const size_t group = (size_t)tpr * E * (kBnStages * arrays + (bwd ? 4 : 0)), vecs = (size_t)tpr * E * 12;
-      const size_t block = bwd ? kSmem : kSmem / fwd_blocks(E);
+      const size_t block = bwd ? kMostSmem : kMostSmem / fwd_blocks(E);
       if (vecs + groups * group > block) groups = block > vecs ? (int)((block - vecs) / group) : 1;
     }
+    if (tpr < 32) groups -= groups % (32 / tpr);  // whole warps
     if (groups < 1) groups = 1;
   }
 };

@@ -10,6 +10,8 @@ a mean over D elements adds up at most 16 numbers per thread, 5 shuffle steps an
 K = 128 covers their sum with room; it multiplies the sum of the magnitudes of an output's
 terms.  A weight's gradient is a sum over n rows in fp32: at most n more roundings per term.
 """
+from concurrent.futures import ThreadPoolExecutor
+
 import pytest
 import torch
 
@@ -329,6 +331,38 @@ def test_results_repeat_bit_for_bit_also_on_another_stream():
     b = prism.block_norm_bwd(x_out, args[5], args[7], dx_out=args[8], stream=s, **args[6])
     s.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(first, [y, x_out, h, *a.values(), *b.values()]))
+
+
+def test_two_threads_call_at_once():
+    # the same kernels with different amounts of shared memory, from two host threads
+    sizes = [(("fp32", "bf16"), 768), (("fp32", "fp32"), 1024), (("bf16", "bf16"), 768), (("fp32", "fp32"), 640)]
+    work, want = [], []
+    for (stream, dtype), D in sizes:
+        x, w, vec, dh, dxo = _block_inputs(2, 300, D, stream, dtype, True, True, True, D)
+        args = (x.cuda(), w.cuda(), dh.cuda(), dxo.cuda(), {n: t.cuda() for n, t in vec.items()})
+        work.append(args)
+    torch.cuda.synchronize()
+
+    def run(args, s=None):
+        x, w, dh, dxo, v = args
+        fwd = prism.block_norm_fwd(x, w, stream=s, **v)
+        return [*fwd, *prism.block_norm_bwd(x, w, dh, dx_out=dxo, stream=s, **v).values()]
+
+    want = [run(a) for a in work]
+    torch.cuda.synchronize()
+
+    def many(mine):
+        s = torch.cuda.Stream()
+        out = [[run(a, s) for a in mine] for _ in range(40)]
+        s.synchronize()
+        return out
+
+    with ThreadPoolExecutor(2) as pool:
+        jobs = [pool.submit(many, work[:2]), pool.submit(many, work[2:])]
+        for k, job in enumerate(jobs):
+            for out in job.result():
+                for a, b in zip(out, want[2 * k:2 * k + 2]):
+                    assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
 def test_a_captured_graph_follows_its_inputs():
