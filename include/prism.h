@@ -456,8 +456,8 @@ int prism_embed_fwd(const void* ids, const void* table, const int32_t* lengths, 
  *   the sums are added to what d_table holds and only the rows that a token names are touched
  * Ids outside [0, V) give no gradient and are recorded as in prism_embed_fwd.  workspace: at
  * least prism_embed_bwd_workspace_size() bytes (16 bytes a token for the sorted ids, up to 2 MB
- * of counts, and 8 D bytes for each chunk of 16 to 128 tokens).  Three launches for up to 32768
- * tokens, else five to nine.
+ * of counts, a bit per table row, and 8 D bytes for each chunk of 16 to 128 tokens).  Three or
+ * four launches for up to 32768 tokens, else five to eleven.
  */
 size_t prism_embed_bwd_workspace_size(int B, int T, int V, int D);
 

@@ -21,6 +21,7 @@ struct EmbedParams {
   uint2* pairs[2];    // backward workspace: (id, token) pairs, the passes' outputs in turn
   int* hist;          // [passes, tiles, bins]: a digit's pairs of a tile, then those of earlier tiles
   int* totals;        // [passes, bins]: a digit's pairs
+  uint32_t* present;  // dense gradient: one bit per table row, set where a token names it
   float* part;        // [chunks, 2, D]
   long long N;        // B T < 2^31
   FastDiv T;
@@ -35,7 +36,7 @@ struct EmbedPlan {
   int cluster, kpt;    // blocks of the one-launch sort (0: by tiles); pairs per thread of a round
   int tile, tiles;     // tokens of a sorting block; blocks
   int chunk, chunks;   // sorted positions that one thread group sums; groups
-  size_t off_hist, off_totals, off_part, off_pairs[2], bytes;
+  size_t off_hist, off_totals, off_present, off_part, off_pairs[2], bytes;
   EmbedPlan(long long N, int V, int D) {
     int bits = 1;
     while (bits < 31 && (V >> bits) != 0) ++bits;  // the keys are 0 .. V
@@ -64,6 +65,7 @@ struct EmbedPlan {
     for (size_t& off : off_pairs) { off = bytes; bytes += al((size_t)N * 8); }
     off_hist = bytes; bytes += al(((size_t)passes * tiles << digit) * 4);
     off_totals = bytes; bytes += al(((size_t)passes << digit) * 4);
+    off_present = bytes; bytes += al(((size_t)V + 31) / 32 * 4);
     off_part = bytes; bytes += al((size_t)chunks * 2 * D * 4);
   }
 };

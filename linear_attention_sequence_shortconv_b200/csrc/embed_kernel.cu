@@ -24,6 +24,8 @@
 // 1000003 x 128: 48 us (floor 11).
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "embed.cuh"
 #include "rowops.cuh"
 
@@ -75,6 +77,17 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(EmbedParams p, i
 // ------------------------------------------------------------------------------------ the sort
 constexpr int kMaxBins = 1 << kEmbedMaxDigit;
 constexpr uint32_t kNoKey = 0xffffffffu;  // a place behind the last token
+
+// The bits of the table rows that a token names (dense gradients only): cleared by the first
+// sorting launch, set once per block or run.
+__device__ __forceinline__ void clear_present(const EmbedParams& p, int block, int blocks) {
+  if (!p.present) return;
+  const int words = (int)(((long long)p.V + 31) / 32);
+  for (int i = block * blockDim.x + threadIdx.x; i < words; i += blocks * blockDim.x) p.present[i] = 0;
+}
+__device__ __forceinline__ void set_present(const EmbedParams& p, uint32_t key) {
+  if (p.present && key < (uint32_t)p.V) atomicOr(p.present + key / 32, 1u << key % 32);
+}
 
 // Stable ranks of a warp's 32 * KPT consecutive keys among the equal digits of the warp, and
 // the warp's counts per digit (`count`, zero before).  The lanes of equal digit are found by one
@@ -178,6 +191,7 @@ __global__ void __launch_bounds__(kClusterThreads) sort_cluster_kernel(EmbedPara
   const long long block0 = (long long)me * kClusterThreads * KPT, first = block0 + warp * 32 * KPT + lane;
   const int mine = (int)(p.N - block0 < kClusterThreads * KPT ? (p.N > block0 ? p.N - block0 : 0) : kClusterThreads * KPT);
   launch_dependents();
+  clear_present(p, me, blocks);
   for (int pass = 0; pass < plan.passes; ++pass) {
     const int shift = pass * plan.digit;
     const uint2* in = pass & 1 ? p.pairs[0] : p.pairs[1];
@@ -233,6 +247,8 @@ __global__ void __launch_bounds__(kClusterThreads) sort_cluster_kernel(EmbedPara
       const uint2 x = staged[i];
       const int at = base[(x.x >> shift) & (bins - 1)] + i;
       if (in_bounds(at, p.N, p.status)) out[at] = x;
+      // in the last pass the staged pairs are in the order of their whole keys
+      if (pass + 1 == plan.passes && (i == 0 || staged[i - 1].x != x.x)) set_present(p, x.x);
     }
     cluster_arrive();  // the pairs are out, and nobody reads this block's counts any more
     cluster_wait();
@@ -249,6 +265,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(EmbedParams p,
   __shared__ int count[kMaxBins];
   const int bins = 1 << plan.digit;
   launch_dependents();
+  clear_present(p, blockIdx.x, gridDim.x);
   for (int i = threadIdx.x; i < bins; i += kSortThreads) count[i] = 0;
   __syncthreads();
   const long long first = (long long)blockIdx.x * plan.tile;
@@ -363,6 +380,16 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(EmbedParams p, 
   }
 }
 
+// The rows' bits, from the sorted pairs of the tiles.
+__device__ __forceinline__ const uint2* sorted_pairs(const EmbedParams& p, const EmbedPlan& plan);
+__global__ void __launch_bounds__(kSortThreads) mark_present_kernel(EmbedParams p, EmbedPlan plan) {
+  launch_dependents();
+  wait_for_previous();
+  const uint2* pairs = sorted_pairs(p, plan);
+  const long long i = (long long)blockIdx.x * kSortThreads + threadIdx.x;
+  if (i < p.N && (i == 0 || pairs[i - 1].x != pairs[i].x)) set_present(p, pairs[i].x);
+}
+
 // the last pass's output (no index into the parameters, which would copy them to local memory)
 __device__ __forceinline__ const uint2* sorted_pairs(const EmbedParams& p, const EmbedPlan& plan) {
   return plan.passes & 1 ? p.pairs[0] : p.pairs[1];
@@ -372,9 +399,11 @@ __device__ __forceinline__ const uint2* sorted_pairs(const EmbedParams& p, const
 // Eight columns per thread: consecutive ones where D is a multiple of 8, else one of every
 // tpr.  blockIdx.y is the tile of 8 tpr columns.
 constexpr int kSumThreads = 256;
-constexpr int kZeroRows = 64;  // table rows that one zeroing block looks after
+constexpr int kZeroRows = 64;  // table rows per zeroing block, about
 constexpr int kJoinThreads = 512;
-constexpr int kLongChunks = 8;   // chunks whose long runs one block takes
+constexpr int kFoldFrom = 16384;   // chunks from which that is worth a launch
+constexpr int kLongChunks = 8;    // chunks whose long runs one block of the join takes
+constexpr int kFold = 64;          // partial sums that are folded into one where a run holds them all
 constexpr int kShortRun = 8;   // partial sums behind a run's first up to which one thread group joins it
 
 // Eight columns as they lie in memory.
@@ -443,43 +472,29 @@ struct Columns {
   }
 };
 
-// First position in [0, N) whose key is at least v, found by a warp: 32 probes a step.
-__device__ __forceinline__ int lower_bound(const uint2* pairs, int N, uint32_t v, int lane) {
-  int lo = 0, hi = N;  // the answer is in [lo, hi]
-  while (lo < hi) {
-    const int step = (hi - lo + 32) / 33;  // at least 1
-    const long long at = (long long)lo + (long long)(lane + 1) * step - 1;
-    const bool less = at < hi && pairs[at].x < v;
-    const int n = __popc(__ballot_sync(0xffffffffu, less));  // the keys are sorted: a prefix of the probes
-    const long long top = (long long)lo + (long long)(n + 1) * step - 1;
-    lo += n * step;
-    if (top < hi) hi = (int)top;
-  }
-  return lo;
-}
-
-// table rows [v0, v0 + kZeroRows): those without a token become zero
-__device__ __forceinline__ void zero_absent_rows(const EmbedParams& p, const uint2* pairs, long long v0) {
-  __shared__ int range[2];
-  __shared__ int present[kZeroRows];
-  const int rows = (int)(p.V - v0 < kZeroRows ? p.V - v0 : kZeroRows);
-  if (threadIdx.x < 64) {  // two warps, one for each end
-    const int at = lower_bound(pairs, (int)p.N, (uint32_t)(v0 + (threadIdx.x < 32 ? 0 : rows)), threadIdx.x % 32);
-    if (threadIdx.x % 32 == 0) range[threadIdx.x / 32] = at;
-  }
-  for (int r = threadIdx.x; r < kZeroRows; r += blockDim.x) present[r] = 0;
-  __syncthreads();
-  for (int i = range[0] + threadIdx.x; i < range[1]; i += blockDim.x) present[pairs[i].x - (uint32_t)v0] = 1;
-  __syncthreads();
-  const float zero[8] = {};
-  const bool vec = p.D % 8 == 0;
-  const int pieces = vec ? p.D / 8 : p.D;
-  for (int r = 0; r < rows; ++r) {
-    if (present[r]) continue;
-    float* row = p.d_table + (size_t)(v0 + r) * p.D;
-    for (int c = threadIdx.x; c < pieces; c += blockDim.x) {
-      if (vec) store8(row + 8 * c, zero);
-      else row[c] = 0.f;
+// The table rows without a token become zero: a warp per row, consecutive warps on consecutive
+// rows, so that what is being written at a time lies together (blocks with 64 rows each, 192 KB
+// apart, wrote at 3.5 TB/s).
+__device__ __forceinline__ void zero_absent_rows(const EmbedParams& p, int block, int blocks) {
+  const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
+  if ((int)threadIdx.x >= warps * 32) return;
+  const bool vec = p.D % 4 == 0;
+  const int pieces = vec ? p.D / 4 : p.D;
+  const long long step = (long long)blocks * warps;
+  constexpr int kRows = 8;  // whose bits are read before the first is written
+  for (long long r0 = (long long)block * warps + threadIdx.x / 32; r0 < p.V; r0 += step * kRows) {
+    uint32_t bits[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) bits[i] = r0 + i * step < p.V ? p.present[(r0 + i * step) / 32] : ~0u;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const long long r = r0 + i * step;
+      if (bits[i] >> (r % 32) & 1) continue;
+      float* row = p.d_table + (size_t)r * p.D;
+      for (int c = lane; c < pieces; c += 32) {
+        if (vec) reinterpret_cast<float4*>(row)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        else row[c] = 0.f;
+      }
     }
   }
 }
@@ -494,7 +509,7 @@ __global__ void __launch_bounds__(kSumThreads, 3) embed_sum_kernel(EmbedParams p
   launch_dependents();
   wait_for_previous();
   if ((int)blockIdx.x < zero_blocks) {
-    if (blockIdx.y == 0) zero_absent_rows(p, pairs, (long long)blockIdx.x * kZeroRows);
+    if (blockIdx.y == 0) zero_absent_rows(p, blockIdx.x, zero_blocks);
     return;
   }
   const long long block = blockIdx.x - zero_blocks;
@@ -574,6 +589,29 @@ struct Runs {
   }
 };
 
+// A run of up to kShortRun further partial sums that begins in chunk c: one thread group adds
+// them from left to right.
+template <bool VEC>
+__device__ __forceinline__ void join_short_run(const EmbedParams& p, const Runs& runs, const Columns<VEC>& col, long long c) {
+  float acc[8], x[8];
+  uint32_t far, key[kShortRun];
+#pragma unroll
+  for (int n = 0; n < kShortRun; ++n) key[n] = runs.at(c + 1 + n);
+  const uint32_t id = runs.begins(c, &far);
+  if (id == runs.none || far == id) return;
+  int heads = 0;
+#pragma unroll
+  for (int n = 0; n < kShortRun; ++n) heads += key[n] == id;
+  col.load(p.part + ((size_t)c * 2 + 1) * p.D, acc);
+#pragma unroll 4
+  for (int n = 1; n <= heads; ++n) {
+    col.load(p.part + (size_t)(c + n) * 2 * p.D, x);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] += x[q];
+  }
+  col.finish(p, id, acc);
+}
+
 // A group of `width` threads (up to a warp's) holds 8 width columns; blockIdx.y is their tile.
 // Blocks below `short_blocks`: one group per chunk adds a run of up to kShortRun further partial
 // sums from left to right.  Further blocks look after kLongChunks chunks each and take the
@@ -590,24 +628,7 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(EmbedParams p,
   float acc[8], x[8];
   wait_for_previous();
   if ((int)blockIdx.x < short_blocks) {
-    if (group >= groups) return;
-    const long long c = (long long)blockIdx.x * groups + group;
-    uint32_t far, key[kShortRun];
-#pragma unroll
-    for (int n = 0; n < kShortRun; ++n) key[n] = runs.at(c + 1 + n);
-    const uint32_t id = runs.begins(c, &far);
-    if (id == runs.none || far == id) return;
-    int heads = 0;
-#pragma unroll
-    for (int n = 0; n < kShortRun; ++n) heads += key[n] == id;
-    col.load(p.part + ((size_t)c * 2 + 1) * p.D, acc);
-#pragma unroll 4
-    for (int n = 1; n <= heads; ++n) {
-      col.load(p.part + (size_t)(c + n) * 2 * p.D, x);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) acc[q] += x[q];
-    }
-    col.finish(p, id, acc);
+    if (group < groups) join_short_run<VEC>(p, runs, col, (long long)blockIdx.x * groups + group);
     return;
   }
   const int slices = groups < 32 ? groups : 32;
@@ -650,6 +671,109 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(EmbedParams p,
       col.finish(p, id, acc);
     }
     __syncthreads();
+  }
+}
+
+// Adds rows at(lo) .. at(hi - 1) of the partial sums, dealt out to `slices` groups of the block in
+// equal runs, from left to right; the sum is group 0's.
+template <bool VEC, typename At>
+__device__ __forceinline__ void block_sum(const EmbedParams& p, const Columns<VEC>& col, int width, int slices, int n,
+                                          At at, float (*slice)[9], float (&acc)[8]) {
+  const int group = threadIdx.x / width, gt = threadIdx.x - group * width;
+  float x[8];
+  zero8(acc);
+  if (group < slices) {
+    const int lo = (int)((long long)n * group / slices), hi = (int)((long long)n * (group + 1) / slices);
+#pragma unroll 8
+    for (int i = lo; i < hi; ++i) {
+      col.load(p.part + (size_t)at(i) * p.D, x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[q] += x[q];
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) slice[threadIdx.x][q] = acc[q];
+  __syncthreads();
+  if (group == 0) {
+    for (int g = 1; g < slices; ++g) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[q] += slice[g * width + gt][q];
+    }
+  }
+  __syncthreads();
+}
+
+// Where there are many chunks: the heads of chunks 64 k .. 64 k + 63 become one (in the place of
+// the first) where they all belong to one run, so that no block of the join adds thousands.
+template <bool VEC>
+__global__ void __launch_bounds__(kJoinThreads) embed_fold_kernel(EmbedParams p, EmbedPlan plan, int width) {
+  __shared__ float slice[kJoinThreads][9];  // the ninth only spreads the banks
+  const Runs runs{sorted_pairs(p, plan), (uint32_t)p.V, plan.chunk, plan.chunks};
+  launch_dependents();
+  wait_for_previous();
+  const long long c = (long long)blockIdx.x * kFold;
+  const uint32_t id = runs.at(c + kFold - 1);
+  if (c == 0 || id == runs.none || runs.at(c) != id || runs.pairs[c * plan.chunk - 1].x != id) return;
+  const int groups = kJoinThreads / width;
+  const Columns<VEC> col(threadIdx.x % width, width, blockIdx.y, p.D);
+  float acc[8];
+  block_sum<VEC>(p, col, width, groups < 16 ? groups : 16, kFold, [&](int i) { return (c + i) * 2; }, slice, acc);
+  if (threadIdx.x < width) col.store(p.part + (size_t)c * 2 * p.D, acc);
+}
+
+// The join of many chunks: further blocks look after `per` chunks each, and the heads have been
+// folded.  (With few chunks it takes 15 us where embed_join_kernel takes 11; of 31250 chunks in
+// two runs that one took 275 us.)
+template <bool VEC>
+__global__ void __launch_bounds__(kJoinThreads, 3) embed_join_many_kernel(EmbedParams p, EmbedPlan plan, int width,
+                                                                  int short_blocks, int per) {
+  __shared__ uint32_t found[kJoinThreads / 32], ids[kJoinThreads];
+  __shared__ float slice[kJoinThreads][9];
+  const Runs runs{sorted_pairs(p, plan), (uint32_t)p.V, plan.chunk, plan.chunks};
+  const int groups = kJoinThreads / width, group = threadIdx.x / width, gt = threadIdx.x - group * width;
+  const Columns<VEC> col(gt, width, blockIdx.y, p.D);
+  float acc[8];
+  wait_for_previous();
+  if ((int)blockIdx.x < short_blocks) {
+    if (group < groups) join_short_run<VEC>(p, runs, col, (long long)blockIdx.x * groups + group);
+    return;
+  }
+  const long long c0 = (long long)(blockIdx.x - short_blocks) * per;
+  {
+    uint32_t far = runs.none;
+    const bool mine = (int)threadIdx.x < per;
+    const uint32_t own = mine ? runs.begins(c0 + threadIdx.x, &far) : runs.none;
+    const uint32_t some = __ballot_sync(0xffffffffu, own != runs.none && far == own);
+    if (threadIdx.x % 32 == 0) found[threadIdx.x / 32] = some;
+    ids[threadIdx.x] = own;
+  }
+  __syncthreads();
+  for (int f = 0; f < kJoinThreads / 32; ++f) {
+    for (uint32_t left = found[f]; left; left &= left - 1) {
+      const int k = 32 * f + __ffs(left) - 1;
+      const long long c = c0 + k;
+      const uint32_t id = ids[k];
+      // the chunks behind c that the run reaches are [c + 1, end): all threads probe, the next ones
+      // first, then the rest at equal distances
+      int lo = (int)c + 1, hi = plan.chunks, step = 1;
+      while (lo < hi) {
+        const int at = lo + ((int)threadIdx.x + 1) * step - 1;
+        const int n = __syncthreads_count(at < hi && runs.at(at) == id);  // the keys are sorted: the first n probes
+        const long long top = lo + (long long)(n + 1) * step - 1;
+        lo += n * step;
+        if (n < kJoinThreads && top < hi) hi = (int)top;
+        step = (hi - lo + kJoinThreads) / (kJoinThreads + 1);  // at least 1 while lo < hi
+      }
+      // the tail of c, then the heads: one by one, or by folded groups where the run holds them
+      const int first = (int)c + 1, end = lo;
+      int a = (first + kFold - 1) / kFold * kFold, b = end / kFold * kFold;
+      if (a >= b) a = b = end;
+      const int n1 = a - first, n2 = n1 + (b - a) / kFold, n = 1 + n2 + (end - b);
+      block_sum<VEC>(p, col, width, groups < 64 ? groups : 64, n, [&](int i) {
+        return i == 0 ? 2ll * first - 1 : 2ll * (i <= n1 ? first + i - 1 : i <= n2 ? a + (i - 1 - n1) * kFold : b + (i - 1 - n2));
+      }, slice, acc);
+      if (group == 0) col.finish(p, id, acc);
+    }
   }
 }
 
@@ -707,6 +831,9 @@ cudaError_t sort_tiles(const EmbedParams& p, const EmbedPlan& plan, cudaStream_t
     if (err == cudaSuccess)
       err = launch_chained(sort_pass_kernel<I, KPT>, dim3(plan.tiles), kSortThreads, 0, stream, p, plan, pass);
   }
+  if (err == cudaSuccess && p.present)
+    err = launch_chained(mark_present_kernel, dim3((int)((p.N + kSortThreads - 1) / kSortThreads)), kSortThreads, 0, stream,
+                         p, plan);
   return err;
 }
 
@@ -725,15 +852,23 @@ cudaError_t embed_sums(const EmbedParams& p, const EmbedPlan& plan, cudaStream_t
   const int most = 4096 / plan.chunk, fit = kSumThreads / tpr, groups = fit < most ? fit : most;
   const int tiles = (need + tpr - 1) / tpr, threads = tpr * groups < 64 ? 64 : tpr * groups;
   const int sum_blocks = (plan.chunks + groups - 1) / groups;
-  const int zero_blocks = p.accumulate ? 0 : (int)(((long long)p.V + kZeroRows - 1) / kZeroRows);
+  const int zero_blocks = p.accumulate ? 0 : (int)std::min<long long>(8 * kSMs, ((long long)p.V + kZeroRows - 1) / kZeroRows);
   cudaError_t err = launch_chained(embed_sum_kernel<T, VEC>, dim3(sum_blocks + zero_blocks, tiles), threads,
                                    (size_t)groups * plan.chunk * 8, stream, p, plan, tpr, groups, zero_blocks);
   if (err != cudaSuccess || plan.chunks == 1) return err;
-  const int width = need < 32 ? need : 32, joins = kJoinThreads / width;
+  const int width = need < 32 ? need : 32, joins = kJoinThreads / width, slabs = (need + width - 1) / width;
   const int short_blocks = (plan.chunks + joins - 1) / joins;
+  if (plan.chunks > kFoldFrom) {
+    err = launch_chained(embed_fold_kernel<VEC>, dim3(plan.chunks / kFold, slabs), kJoinThreads, 0, stream, p, plan, width);
+    if (err != cudaSuccess) return err;
+    // few chunks per block where there are few, since a block takes its long runs one by one
+    const int per = std::min(std::max(plan.chunks / (8 * kSMs), 8), kJoinThreads);
+    return launch_chained(embed_join_many_kernel<VEC>, dim3(short_blocks + (plan.chunks + per - 1) / per, slabs),
+                          kJoinThreads, 0, stream, p, plan, width, short_blocks, per);
+  }
   const int long_blocks = plan.chunks > kShortRun + 1 ? (plan.chunks + kLongChunks - 1) / kLongChunks : 0;
-  return launch_chained(embed_join_kernel<VEC>, dim3(short_blocks + long_blocks, (need + width - 1) / width),
-                        kJoinThreads, 0, stream, p, plan, width, short_blocks);
+  return launch_chained(embed_join_kernel<VEC>, dim3(short_blocks + long_blocks, slabs), kJoinThreads, 0, stream, p, plan,
+                        width, short_blocks);
 }
 
 }  // namespace

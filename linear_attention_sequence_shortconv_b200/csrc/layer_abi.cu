@@ -263,6 +263,7 @@ int prism_embed_bwd(const void* ids, const void* d_out, const int32_t* lengths, 
   for (int i = 0; i < 2; ++i) p.pairs[i] = reinterpret_cast<uint2*>(ws + plan.off_pairs[i]);
   p.hist = reinterpret_cast<int*>(ws + plan.off_hist);
   p.totals = reinterpret_cast<int*>(ws + plan.off_totals);
+  p.present = accumulate ? nullptr : reinterpret_cast<uint32_t*>(ws + plan.off_present);
   p.part = reinterpret_cast<float*>(ws + plan.off_part);
   p.N = (long long)n;
   p.T = prism::FastDiv(T);

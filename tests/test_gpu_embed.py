@@ -59,6 +59,9 @@ CASES = [
     (1, 200001, 3000, 16, "fp32", "bf16", 32, "zipf", None),       # longer: sorted by tiles
     (3, 100000, 1 << 20, 8, "fp32", "bf16", 64, "zipf", [100000, 1, 77777]),
     (1, 300000, 1, 8, "bf16", "bf16", 32, "one", None),
+    (1, 300001, 2, 16, "fp32", "bf16", 32, "zipf", None),           # thousands of chunks in one run: folded
+    (2, 100000, 40, 64, "fp32", "fp32", 64, "zipf", [100000, 99999]),
+    (1, 280000, 7, 9, "fp32", "bf16", 32, "zipf", [279999]),
 ]
 
 

@@ -134,10 +134,10 @@ def test_workspace_sizes():
     # partial sums: a bounded number of blocks, whatever the length of the batch
     assert L.prism_gated_norm_bwd_workspace_size(1 << 10, 1 << 14, 8, 128) <= 1 << 20
     assert L.prism_block_norm_bwd_workspace_size(1 << 10, 1 << 14, 768) <= 32 << 20
-    # 16 bytes a token, the counts, and two rows for each chunk of at least 16 sorted tokens
+    # 16 bytes a token, the counts, a bit per row, and two rows for each chunk of at least 16 sorted tokens
     for B, T, V, D in ((1, 1, 1, 1), (16, 2048, 32000, 768), (128, 1024, 1000003, 128), (1, 1 << 22, 1 << 30, 64)):
         need, N = L.prism_embed_bwd_workspace_size(B, T, V, D), B * T
-        assert 16 * N <= need <= 16 * N + (2 << 20) + 8 * D * (N // 16 + 1) + 2048
+        assert 16 * N <= need <= 16 * N + (2 << 20) + V // 8 + 8 * D * (N // 16 + 1) + 2048
 
 
 def _adam(tensors, step=1, step_dev=None, lr=1e-3, lr_dev=None, b1=0.9, b2=0.99, eps=1e-8, gs=None, p=1, g=1, bits=32,
