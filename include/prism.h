@@ -414,7 +414,8 @@ int prism_gated_norm_bwd(const void* o, const void* gate, const float* weight, c
  *   x, x_out  [B,T,D] x_dtype; x_out may be x.  y NULL: x_out is not written, h is the norm of x
  *   y, h      [B,T,D] dtype
  *   weight, post_weight (or NULL), scale (or NULL: 1)  [D] fp32
- * 1 <= D <= PRISM_MAX_WIDTH (any width; multiples of 8 take 16-byte accesses).  x_dtype and
+ * 1 <= D <= PRISM_MAX_WIDTH (any width; multiples of 8, of 4 with an
+ * fp32 stream, take wide accesses).  x_dtype and
  * dtype: both PRISM_BF16, both PRISM_FP32, or an fp32 stream with bf16 blocks.  One launch.
  */
 int prism_block_norm_fwd(const void* x, const void* y, const float* post_weight, const float* scale,

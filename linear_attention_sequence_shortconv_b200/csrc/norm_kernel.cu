@@ -242,9 +242,9 @@ __global__ void __launch_bounds__(kGnThreads, 4) gated_norm_bwd_kernel(GatedNorm
 
 // ------------------------------------------------------------------------------ block norm
 // A group of tpr threads holds a row, E columns per thread: tpr is a power of two up to 32,
-// or a multiple of 32.  MAP: kEven8 and kEven4 where D is a multiple of 8 (the threads share 8 tpr
-// columns at a time, in 16-bit rows and where fp32 rows are among them); kOdd otherwise: one
-// column per access, consecutive threads on consecutive columns.
+// or a multiple of 32.  MAP: kEven8 in 16-bit rows where D is a multiple of 8, kEven4 with an
+// fp32 stream where it is one of 4 (the threads share 8 tpr columns at a time); kOdd otherwise:
+// one column per access, consecutive threads on consecutive columns.
 enum Map { kOdd = 0, kEven8 = 1, kEven4 = 2 };
 
 template <int MAP>
@@ -374,10 +374,10 @@ __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d) {
   return x;
 }
 
-template <int N>  // 1 to 4
 struct GroupSum {
   float4 (*buf)[2][kBnThreads / 32];  // [group][parity][warp]
   int parity = 0;
+  template <int N>  // 1 to 4
   __device__ __forceinline__ void run(float (&x)[N], int group, int gt, int tpr) {
     if (tpr <= 32) {
       for (int off = tpr / 2; off > 0; off >>= 1) {
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(fwd_threads(E), fwd_blocks(E)) block_norm_fwd_
   __shared__ float4 buf[kBnGroups][2][kBnThreads / 32];
   extern __shared__ __align__(16) float vecs[];  // weight, k, post_weight: tpr * E each; behind them the ring
   const int tpr = p.tpr, gt = threadIdx.x % tpr, group = threadIdx.x / tpr, D = p.D, n = tpr * E;
-  GroupSum<1> sum{buf};
+  GroupSum sum{buf};
   FwdRows<X, A, E, MAP, DELTA> rows(p, gt, vecs + (1 + DELTA + POST) * n);
   const long long stride = (long long)gridDim.x * p.groups;
   long long row = (long long)blockIdx.x * p.groups + group;
@@ -599,12 +599,10 @@ __global__ void __launch_bounds__(bwd_threads(E, MAP != kOdd), 1)
   constexpr bool Y = POST || SCALE;  // whether y is needed
   constexpr int N = POST ? 3 : 2;
   __shared__ float4 buf[kBnGroups][2][kBnThreads / 32];
-  __shared__ float4 buf1[kBnGroups][2][kBnThreads / 32];
   // weight, k, post_weight: tpr * E each; in the end the groups' column sums; behind them the ring
   extern __shared__ __align__(16) float vecs[];
   const int tpr = p.tpr, gt = threadIdx.x % tpr, group = threadIdx.x / tpr, D = p.D, n = tpr * E;
-  GroupSum<N> sum{buf};
-  GroupSum<1> sum1{buf1};
+  GroupSum sum{buf};
   BwdRows<X, A, E, MAP, Y> rows(p, gt, vecs + max(3, p.groups) * n);
   launch_dependents();
   const long long stride = (long long)gridDim.x * p.groups;
@@ -679,7 +677,7 @@ __global__ void __launch_bounds__(bwd_threads(E, MAP != kOdd), 1)
       }
       if (POST) {
         float c[1] = {c2.x + c2.y};
-        sum1.run(c, group, gt, tpr);
+        sum.run(c, group, gt, tpr);
         const float my = -c[0] * p.inv_D * ry;
 #pragma unroll
         for (int j = 0; j < E / 8; ++j) {
@@ -737,13 +735,16 @@ __global__ void __launch_bounds__(kSumCols * kSumSlices) column_sum_kernel(Colum
   }
 }
 
-constexpr size_t kMostSmem = 216 * 1024;  // dynamic shared memory of a block, beside up to 11 KB of static
+// Dynamic shared memory of a block norm's block, beside 2 KB of static: the only one on its SM, or
+// one of several that share the SM's 228 KB (each takes 1 KB more for itself).
+constexpr size_t kMostSmem = 224 * 1024;
+constexpr size_t smem_share(int blocks) { return 228 * 1024 / blocks - 3 * 1024; }
 
 template <typename... Args>
-cudaError_t launch_with_smem(void (*kernel)(Args...), int blocks, int threads, size_t smem, cudaStream_t stream,
-                             Args... args) {
-  if (smem > 32 * 1024) {  // always the same limit: another thread may be about to launch this kernel
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
+cudaError_t launch_with_smem(void (*kernel)(Args...), size_t most, int blocks, int threads, size_t smem,
+                             cudaStream_t stream, Args... args) {
+  if (smem > 32 * 1024) {  // the kernel's limit is the same in every call: another thread may be launching it too
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (err != cudaSuccess) return err;
   }
   kernel<<<blocks, threads, smem, stream>>>(args...);
@@ -780,10 +781,13 @@ template <typename T, typename Index, int LPR>
 cudaError_t gated_bwd_index(const GatedNormParams& p, int gate, int blocks, cudaStream_t stream) {
   const size_t smem = Ring<3 * Raw8<T>::kPieces, kStages>::bytes(kGnThreads);
   if (gate == kGateNone)
-    return launch_with_smem(gated_norm_bwd_kernel<T, Index, LPR, kGateNone>, blocks, kGnThreads, smem, stream, p);
+    return launch_with_smem(gated_norm_bwd_kernel<T, Index, LPR, kGateNone>, smem, blocks, kGnThreads, smem, stream,
+                            p);
   if (gate == kGateSilu)
-    return launch_with_smem(gated_norm_bwd_kernel<T, Index, LPR, kGateSilu>, blocks, kGnThreads, smem, stream, p);
-  return launch_with_smem(gated_norm_bwd_kernel<T, Index, LPR, kGateSigmoid>, blocks, kGnThreads, smem, stream, p);
+    return launch_with_smem(gated_norm_bwd_kernel<T, Index, LPR, kGateSilu>, smem, blocks, kGnThreads, smem, stream,
+                            p);
+  return launch_with_smem(gated_norm_bwd_kernel<T, Index, LPR, kGateSigmoid>, smem, blocks, kGnThreads, smem, stream,
+                          p);
 }
 
 template <typename T, int LPR>
@@ -795,16 +799,16 @@ cudaError_t gated_bwd_lanes(const GatedNormParams& p, int gate, int blocks, cuda
 // How the block norm is cut: E columns per thread, tpr threads per row, `groups` rows at a time
 // per block.  A warp holds a row of up to 1024 columns, so that no barrier stands between its
 // sums (the 130M-LM backward with 96 threads a row and two barriers: 120 us; with a warp: 60).
-// Widths that are not a multiple of 8, or whose rings would not fit the shared memory, take
-// one column per access.
+// Widths that are not a multiple of 8 (4 with an fp32 stream), or whose rings would not fit the
+// shared memory, take one column per access, at a third of the rate.
 struct BlockShape {
   int E, tpr, groups;
   bool vec;
   BlockShape(int D, bool bwd, int x_bytes, int bytes) {
     const int arrays = (bwd ? 2 : 1) * (x_bytes + bytes);  // bytes of a column that the ring holds per row
     const size_t row = (size_t)((D + 1023) / 1024 * 1024) * (kBnStages * arrays);
-    vec = D % 8 == 0 && row + (size_t)(D + 1023) / 1024 * 1024 * 12 <= kMostSmem;
-    if (bwd) E = D <= 1024 && vec ? (D + 255) / 256 * 8 : vec ? 32 : D <= 4096 ? 8 : 16;
+    vec = D % (x_bytes == 4 ? 4 : 8) == 0 && row + (size_t)(D + 1023) / 1024 * 1024 * 12 <= kMostSmem;
+    if (bwd) E = D <= 1024 && vec ? (D + 255) / 256 * 8 : vec ? 16 : D <= 4096 ? 8 : 16;
     else E = D <= 1024 ? (D + 255) / 256 * 8 : 16;
     const int t = (D + E - 1) / E, most = bwd ? bwd_threads(E, vec) : fwd_threads(E);
     tpr = 1;
@@ -814,7 +818,7 @@ struct BlockShape {
     if (tpr > 32 && groups > kBnGroups) groups = kBnGroups;
     if (vec) {  // a group's part of the rings and of the backward's column sums
       const size_t group = (size_t)tpr * E * (kBnStages * arrays + (bwd ? 4 : 0)), vecs = (size_t)tpr * E * 12;
-      const size_t block = bwd ? kMostSmem : kMostSmem / fwd_blocks(E);
+      const size_t block = bwd ? kMostSmem : smem_share(fwd_blocks(E));
       if (vecs + groups * group > block) groups = block > vecs ? (int)((block - vecs) / group) : 1;
     }
     if (tpr < 32) groups -= groups % (32 / tpr);  // whole warps
@@ -827,7 +831,8 @@ cudaError_t block_fwd_kernel(const BlockNormParams& p, int blocks, cudaStream_t 
   const int threads = p.tpr * p.groups;
   const size_t vecs = (size_t)(1 + DELTA + POST) * p.tpr * E * 4;
   const size_t ring = (size_t)FwdRows<X, A, E, MAP, DELTA>::kAll * 16 * kBnStages * threads;
-  return launch_with_smem(block_norm_fwd_kernel<X, A, E, MAP, DELTA, POST>, blocks, threads, vecs + ring, stream, p);
+  return launch_with_smem(block_norm_fwd_kernel<X, A, E, MAP, DELTA, POST>, kMostSmem, blocks, threads, vecs + ring,
+                          stream, p);
 }
 
 template <typename X, typename A, int E, int MAP>
@@ -842,8 +847,8 @@ cudaError_t block_bwd_kernel(const BlockNormParams& p, int blocks, cudaStream_t 
   const int threads = p.tpr * p.groups;
   const size_t vecs = (size_t)(p.groups > 3 ? p.groups : 3) * p.tpr * E * 4;
   const size_t ring = (size_t)BwdRows<X, A, E, MAP, POST || SCALE>::kAll * 16 * kBnStages * threads;
-  return launch_with_smem(block_norm_bwd_kernel<X, A, E, MAP, DELTA, POST, SCALE>, blocks, threads, vecs + ring, stream,
-                          p);
+  return launch_with_smem(block_norm_bwd_kernel<X, A, E, MAP, DELTA, POST, SCALE>, kMostSmem, blocks, threads,
+                          vecs + ring, stream, p);
 }
 
 template <typename X, typename A, int E, int MAP>

@@ -194,6 +194,14 @@ BLOCK = [
     (3, 131, 768, "fp32", "bf16", True, True, True, 1.0, [131, 0, 64]),
     (2, 997, 768, "bf16", "bf16", True, True, True, 1.0, None),
     (3, 97, 1001, "fp32", "fp32", True, False, False, 1.0, [97, 1, 96]),
+    (2, 60, 12, "fp32", "bf16", True, True, True, 1.0, [60, 7]),
+    (2, 60, 100, "fp32", "fp32", True, True, True, 1.0, None),
+    (2, 60, 100, "bf16", "bf16", True, False, True, 1.0, [3, 60]),
+    (1, 50, 1028, "fp32", "bf16", True, True, True, 1.0, [49]),
+    (1, 30, 1536, "bf16", "bf16", True, True, True, 1.0, None),
+    (1, 200, 8192, "bf16", "bf16", True, True, True, 1.0, [199]),
+    (1, 180, 5120, "fp32", "fp32", True, True, True, 1.0, None),
+    (1, 400, 2048, "bf16", "bf16", True, True, False, 0.5, None),
     (1, 40, 1024, "bf16", "bf16", True, False, False, 1.0, None),
     (1, 21, 2056, "fp32", "bf16", True, True, True, 1.0, [20]),
     (1, 9, 4095, "fp32", "bf16", True, True, True, 1.0, None),
