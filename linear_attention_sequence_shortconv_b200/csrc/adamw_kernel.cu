@@ -15,7 +15,7 @@
 //
 // Measured over the 145 tensors (110 M elements) of a 12-layer model of width 768, fp32
 // parameters with bf16 copies: fp32 states and gradients 500 us, 6.6 TB/s, the rate of a copy;
-// 8-bit states and bf16 gradients 359 us, 4.9 TB/s (75%): some 50 instructions an element (two
+// 8-bit states and bf16 gradients 358 us, 4.9 TB/s (75%): some 50 instructions an element (two
 // roots and conversions both ways among them) share the time with the memory.
 #include "adamw.cuh"
 #include "rowops.cuh"

@@ -12,16 +12,18 @@
 // equal length, each thread group walks one chunk with its columns in registers and writes
 // every run that lies inside the chunk; a run that crosses a chunk's border leaves partial
 // sums, which a last launch adds in a fixed order.  No floating-point atomics, so the result
-// does not depend on any order of execution.  Rows without a token are written as zero by
-// further blocks of the summing launch, so a dense gradient is written exactly once.
+// does not depend on any order of execution.  Very many chunks have the partial sums of long runs
+// folded in between.  Rows without a token (a bitmap that the sort leaves) are written as zero
+// by further blocks of the summing launch, so a dense gradient is written exactly once.
 //
 // The lookup is bound by memory (recommendation batch, 128 x 1024 ragged tokens, a table of
 // 1000003 x 128 in fp32: 12 us, 4.1 TB/s).  The gradient reads d_out once and writes the table's
 // gradient once, but about half of its time is a chain of steps that each wait for the one
 // before: with rows of 8 elements, where there is nothing to move, 32768 tokens take 33 us (sort
 // 13.5, sums 14, joins 8, less what the chained launches overlap).  Measured: 130M LM, 32768
-// tokens, dense gradient of 32000 x 768: 55 us (floor 22.7); recommendation batch, added to
-// 1000003 x 128: 48 us (floor 11).
+// tokens, dense gradient of 32000 x 768: 56 us (floor 22.7); recommendation batch, added to
+// 1000003 x 128: 49 us (floor 11); a million tokens over two rows of 64: 71 us (without the
+// fold 1154), over 3000: 118 us (searching the sorted keys for rows without a token: 205).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -401,10 +403,10 @@ __device__ __forceinline__ const uint2* sorted_pairs(const EmbedParams& p, const
 constexpr int kSumThreads = 256;
 constexpr int kZeroRows = 64;  // table rows per zeroing block, about
 constexpr int kJoinThreads = 512;
-constexpr int kFoldFrom = 16384;   // chunks from which that is worth a launch
-constexpr int kLongChunks = 8;    // chunks whose long runs one block of the join takes
+constexpr int kLongChunks = 8;     // chunks whose long runs one block of the join takes
 constexpr int kFold = 64;          // partial sums that are folded into one where a run holds them all
-constexpr int kShortRun = 8;   // partial sums behind a run's first up to which one thread group joins it
+constexpr int kFoldFrom = 16384;   // chunks from which that is worth a launch
+constexpr int kShortRun = 8;       // partial sums behind a run's first up to which one thread group joins it
 
 // Eight columns as they lie in memory.
 template <typename T>

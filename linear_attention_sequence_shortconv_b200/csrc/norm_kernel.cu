@@ -19,9 +19,9 @@
 //
 // Measured on a B200 in a loop over three sets of tensors, with the share of the copy rate of
 // 6.56 TB/s: gated norm, 130M-LM layer (B 16, T 2048, H 6, d 128, bf16, strided gate) forward
-// 29 us, 79%; recommendation layer (B 128, T 1024, H 2, d 64, ragged) backward 27 us, 71%;
+// 29 us, 79%; recommendation layer (B 128, T 1024, H 2, d 64, ragged) backward 27 us, 72%;
 // block norm, 130M LM (B 16, T 2048, D 768) forward with an fp32 stream 58 us, 80%, backward in
-// bf16 60 us, 76%.  What was in the way before the memory: the instructions (half of what is
+// bf16 61 us, 75%.  What was in the way before the memory: the instructions (half of what is
 // left are conversions, sums and exponentials, in packed pairs where the hardware has them),
 // and 32-byte sectors moved in two halves.
 #include "rowops.cuh"
