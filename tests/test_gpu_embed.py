@@ -169,6 +169,20 @@ def test_a_captured_graph_follows_its_inputs():
         assert torch.equal(grad, prism.embed_bwd(ids, d, V, lengths=lens))
 
 
+@pytest.mark.parametrize("V,D", [(1, 1), (31, 1), (33, 2), (1000, 3), (4097, 11), (500, 24), (129, 232), (67, 257),
+                                 (35, 510), (70, 512), (41, 1025)])
+@pytest.mark.parametrize("share", [0.0, 0.02, 0.6, 1.0])
+def test_every_row_without_a_token_is_zero_and_no_other(V, D, share):
+    rows = torch.randperm(V, generator=_gen(8))[:max(1, int(share * V))]
+    ids = rows.repeat(2).view(1, -1)
+    dirty = torch.full((V + 1, D), float("nan"), device="cuda")
+    d = torch.randint(1, 9, (1, ids.shape[1], D), generator=_gen(9)).float()  # their sums are exact
+    got = prism.embed_bwd(ids.cuda(), d.cuda(), V, d_table=dirty[:V])
+    want = torch.zeros(V, D).index_add_(0, ids.view(-1), d.view(-1, D))
+    assert torch.equal(got.cpu(), want)
+    assert dirty[V].isnan().all()
+
+
 def test_rows_beyond_two_to_the_31_elements():
     # the last rows of a table of 2^31 + 2^24 elements, read and written
     V, D = (1 << 18) + 2048, 8192
