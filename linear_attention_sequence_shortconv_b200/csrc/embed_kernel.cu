@@ -84,8 +84,9 @@ constexpr uint32_t kNoKey = 0xffffffffu;  // a place behind the last token
 // sorting launch, set once per block or run.
 __device__ __forceinline__ void clear_present(const EmbedParams& p, int block, int blocks) {
   if (!p.present) return;
-  const int words = (int)(((long long)p.V + 31) / 32);
-  for (int i = block * blockDim.x + threadIdx.x; i < words; i += blocks * blockDim.x) p.present[i] = 0;
+  const int pieces = (int)(((long long)p.V + 127) / 128);  // of 16 bytes, as the bitmap's room is
+  for (int i = block * blockDim.x + threadIdx.x; i < pieces; i += blocks * blockDim.x)
+    reinterpret_cast<uint4*>(p.present)[i] = make_uint4(0, 0, 0, 0);
 }
 __device__ __forceinline__ void set_present(const EmbedParams& p, uint32_t key) {
   if (p.present && key < (uint32_t)p.V) atomicOr(p.present + key / 32, 1u << key % 32);
@@ -481,10 +482,11 @@ struct Columns {
 __device__ __forceinline__ void zero_absent_rows(const EmbedParams& p, FastDiv D, int block, int blocks) {
   const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
   if ((int)threadIdx.x >= warps * 32) return;
-  int rows = 32;  // a power of two, so that a unit's bits are in one word
-  while (rows > 1 && rows * p.D > 1024) rows /= 2;
+  // a power of two, so that a unit's bits are in one word; not below 4 where that aligns a unit
+  int rows = 32;
+  while (rows > (p.D % 4 ? 4 : 1) && rows * p.D > 1024) rows /= 2;
   const uint32_t all = ~0u >> (32 - rows);
-  const bool vec = rows * p.D % 4 == 0, vec_rows = p.D % 4 == 0;
+  const bool vec_rows = p.D % 4 == 0;
   const long long units = ((long long)p.V + rows - 1) / rows, step = (long long)blocks * warps;
   constexpr int kUnits = 8;  // whose bits are read before the first is written
   for (long long u0 = (long long)block * warps + threadIdx.x / 32; u0 < units; u0 += step * kUnits) {
@@ -500,7 +502,7 @@ __device__ __forceinline__ void zero_absent_rows(const EmbedParams& p, FastDiv D
       const long long r = (u0 + i * step) * rows;
       const int n = (int)(p.V - r < rows ? p.V - r : rows) * p.D;  // elements
       float* at = p.d_table + (size_t)r * p.D;
-      if (bits[i] == 0 && vec) {
+      if (bits[i] == 0) {
         for (int c = lane; c < n / 4; c += 32) reinterpret_cast<float4*>(at)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (lane < n % 4) at[n - 1 - lane] = 0.f;
       } else if (vec_rows) {
