@@ -68,19 +68,26 @@ __device__ __forceinline__ float2 sum_of_products(float2 a, float2 b, float2 c, 
   return make_float2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
 }
 
+// p - (lr wd p + update): the decay joins the update before the one rounding to p's precision.  As a
+// factor 1 - lr wd it would itself be rounded, to a step of 2^-24, the same way in every step and for
+// every element (lr wd = 1e-8: no decay at all; 3e-8: twice of it).  An infinite parameter takes the
+// decay of the largest number and stays what it is.
+__device__ __forceinline__ float decayed(float p) { return fminf(fmaxf(p, -3.402823466e38f), 3.402823466e38f); }
+
 __device__ __forceinline__ float updated(float p, float m, float root, const AdamParams& a, const Factors& f,
-                                         float keep) {
-  return p * keep - f.lr_c1 * m / (root * f.rsqrt_c2 + a.eps);
+                                         float decay) {
+  return p - fmaf(decay, decayed(p), f.lr_c1 * m / (root * f.rsqrt_c2 + a.eps));
 }
 
 // The same of two elements with the approximate reciprocal (1 unit of 2^-23): the update is a
 // small part of the parameter, and a root is at most the root of the largest number.
 __device__ __forceinline__ float2 updated2(float2 p, float2 m, float2 root, const AdamParams& a, const Factors& f,
-                                           float keep) {
+                                           float decay) {
   float2 d = fma2(root, both(f.rsqrt_c2), both(a.eps));
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d.x));
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d.y));
-  return fma2(mul2(m, d), both(-f.lr_c1), mul2(p, both(keep)));
+  // p + (-lr wd p - update)
+  return add2(p, fma2(make_float2(decayed(p.x), decayed(p.y)), both(-decay), mul2(mul2(m, d), both(-f.lr_c1))));
 }
 
 template <int N>
@@ -99,7 +106,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw32_kernel(const __grid_cons
                                                                AdamParams a) {
   const AdamTensor& t = find_tensor(table, count);
   const Factors f = step_factors(a);
-  const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.f, keep = 1.f - f.lr * t.weight_decay;
+  const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.f, decay = f.lr * t.weight_decay;
   const long long first = (long long)(blockIdx.x - t.first_block) * kAdamChunk;
   P* p = static_cast<P*>(t.p);
   const G* g = static_cast<const G*>(t.g);
@@ -131,7 +138,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw32_kernel(const __grid_cons
       const float gr = y[e] * gs;
       mm[e] = moment(mm[e], gr, a.b1, a.r1);
       vv[e] = moment(vv[e], __fmul_rn(gr, gr), a.b2, a.r2);
-      x[e] = updated(x[e], mm[e], sqrtf(vv[e]), a, f, keep);
+      x[e] = updated(x[e], mm[e], sqrtf(vv[e]), a, f, decay);
     }
     if (rest == 8) {
       store8(p + i, x);
@@ -253,7 +260,7 @@ struct Stepped8 {
 // zero times a scale that is NaN is not zero).
 template <bool PART, typename P, typename G>
 __device__ __forceinline__ Stepped8 step8(const Loaded8<P, G>& in, const AdamParams& a, const Factors& f, float gs,
-                                          float keep, int lane, int rest) {
+                                          float decay, int lane, int rest) {
   Stepped8 out;
   float2 m[4], r[4];
   decode8(in.m, in.m_scale, m);
@@ -264,7 +271,7 @@ __device__ __forceinline__ Stepped8 step8(const Loaded8<P, G>& in, const AdamPar
     m[i] = sum_of_products(m[i], both(a.b1), g, both(a.r1));
     const float2 v = sum_of_products(mul2(r[i], r[i]), both(a.b2), mul2(g, g), both(a.r2));
     r[i] = make_float2(sqrtf(v.x), sqrtf(v.y));
-    out.x[i] = updated2(in.p.get(i), m[i], r[i], a, f, keep);
+    out.x[i] = updated2(in.p.get(i), m[i], r[i], a, f, decay);
     if (PART) {
       const int e = share<true>(2 * i, lane, 32);
       if (e >= rest) m[i].x = r[i].x = 0.f;
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw8_kernel(const __grid_const
                                                               AdamParams a) {
   const AdamTensor& t = find_tensor(table, count);
   const Factors f = step_factors(a);
-  const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.f, keep = 1.f - f.lr * t.weight_decay;
+  const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.f, decay = f.lr * t.weight_decay;
   const int lane = threadIdx.x % 32, warps = kAdamThreads / 32;
   const int per = a.chunk / kAdamBlock;
   const long long first = (long long)(blockIdx.x - t.first_block) * per;
@@ -296,7 +303,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw8_kernel(const __grid_const
   for (; b < last; b += warps) {
     cur = next;
     if (b + warps < last) next.load(t, b + warps, lane);
-    const Stepped8 s = step8<false>(cur, a, f, gs, keep, lane, kAdamBlock);
+    const Stepped8 s = step8<false>(cur, a, f, gs, decay, lane, kAdamBlock);
     const long long at = b * kAdamBlock;
     store_shared8<true>(p + at, lane, 32, kAdamBlock, s.x);
     if (copy) store_shared8<true>(copy + at, lane, 32, kAdamBlock, s.x);
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw8_kernel(const __grid_const
   const int rest = (int)(t.n - full * kAdamBlock);
   if (b != full || rest == 0 || full >= first + per) return;
   cur.load_part(t, full, lane, rest);
-  const Stepped8 s = step8<true>(cur, a, f, gs, keep, lane, rest);
+  const Stepped8 s = step8<true>(cur, a, f, gs, decay, lane, rest);
   const long long at = full * kAdamBlock;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {

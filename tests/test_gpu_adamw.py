@@ -314,3 +314,43 @@ def test_refusals_name_the_argument():
     with pytest.raises(prism.PrismError, match="UNSUPPORTED"):  # not on 16 bytes
         prism.adamw_step([t[0][1:]], [t[1][1:]], [t[2][1:]], [t[3][1:]])
     assert all(not x.any() for x in t)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("lr,wd", [(1e-4, 1e-4), (1e-4, 3e-4), (1e-4, 1e-3), (1e-4, 1e-2)])
+def test_a_small_decay_is_the_one_asked_for(bits, lr, wd):
+    """lr wd from 1e-8 to 1e-6, where 1 - lr wd in fp32 is up to 100% off: the mean change of many
+    parameters against the one in fp64.
+
+    Every parameter stands twice, with opposite gradients, so that what the mean change holds of
+    the updates is their roundings, at most K 2^-24 of their mean magnitude.  A new parameter in
+    (1, 2) is rounded to a step of 2^-23: over n mantissas and updates that spread over more than
+    500 steps the mean rounding is below 8 standard deviations, 8 step / sqrt(12 n), and
+    1/500 of a step.
+    """
+    n, eps = 1 << 20, 1.0
+    gen = torch.Generator().manual_seed(4)
+    p0 = (1.001 + 0.998 * torch.rand(n // 2, generator=gen)).repeat(2)
+    g0 = 0.5 + 3.5 * torch.rand(n // 2, generator=gen)  # g / (g + eps) from 0.33 to 0.8
+    g0 = torch.cat([g0, -g0])
+    p, state = [p0.cuda()], prism.adamw_state([p0.cuda()], bits=bits)
+    prism.adamw_step(p, [g0.cuda()], step=1, lr=lr, betas=(0.9, 0.95), eps=eps, weight_decay=wd, **state)
+    zero = torch.zeros(n, dtype=torch.float64)
+    want, _, _ = ref.adamw(p0.double(), g0.double(), zero, zero, 1, lr, (0.9, 0.95), eps, wd)
+    update = (p0.double() * (1 - lr * wd) - want).abs().mean().item()
+    step = 2.0 ** -23
+    bound = K * U * (update + 2 * lr * wd) + 8 * step / (12 * n) ** 0.5 + step / 500
+    assert abs((p[0].double().cpu() - want).mean().item()) <= bound
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("wd", [0.0, 0.1])
+def test_infinite_parameters_stay(bits, wd):
+    # such as the entries of a bias that masks
+    p, inf = [torch.full((700,), 0.5, device="cuda")], float("inf")
+    p[0][3], p[0][300], p[0][699] = -inf, inf, -inf
+    prism.adamw_step(p, [torch.zeros(700, device="cuda")], step=1, lr=0.1, weight_decay=wd,
+                     **prism.adamw_state(p, bits=bits))
+    want = torch.full((700,), 0.5 * (1 - 0.1 * wd))
+    want[3], want[300], want[699] = -inf, inf, -inf
+    assert torch.allclose(p[0].cpu(), want, rtol=2 * U, atol=0)
