@@ -23,6 +23,7 @@ PRISM_ACT_SILU = 0
 PRISM_ACT_SIGMOID = 1
 ACTS = {"silu": PRISM_ACT_SILU, "sigmoid": PRISM_ACT_SIGMOID}
 STATE_BLOCK = 256  # elements under one scale of the 8-bit AdamW states
+PRISM_ERR_UNSUPPORTED = 2
 
 
 def _act_code(act: str) -> int:
@@ -79,8 +80,19 @@ def _workspace(workspace, need: int, dev: torch.device):
     return workspace
 
 
+INT_MAX = 0x7FFFFFFF
+
+
+def _fit(what: str, sizes) -> None:
+    """Refuses sizes beyond the C interface's int, which ctypes would cut off without an error."""
+    if any(n > INT_MAX for n in sizes):
+        raise PrismError(PRISM_ERR_UNSUPPORTED, f"{what} with {tuple(sizes)}")
+
+
 def _heads(o: torch.Tensor):
     """Sizes (B, T, H, d) of [B, T, H, d], or of one decoded token [B, H, d]."""
+    if o.numel() > INT_MAX:
+        _fit("o", o.shape)
     if o.dim() == 4:
         return tuple(o.shape)
     if o.dim() == 3:
@@ -165,6 +177,8 @@ def gated_norm_bwd(o, gate, weight, dy, lengths=None, eps: float = 1e-5, act: st
 
 def _stream_rows(x: torch.Tensor):
     """Sizes (B, T, D) of [B, T, D], or of one decoded token [B, D]."""
+    if x.numel() > INT_MAX:
+        _fit("x", x.shape)
     if x.dim() == 3:
         return tuple(x.shape)
     if x.dim() == 2:
@@ -251,8 +265,17 @@ def _id_sizes(ids: torch.Tensor, lengths):
         raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
     if ids.dim() not in (1, 2):
         raise ValueError(f"ids must be [B, T] or [B], got {tuple(ids.shape)}")
+    if ids.numel() > INT_MAX:
+        _fit("ids", ids.shape)
     B, T = ids.shape if ids.dim() == 2 else (ids.shape[0], 1)
     return B, T, 32 if ids.dtype == torch.int32 else 64
+
+
+def _table_sizes(V: int, D: int):
+    """(V, D) of an embedding table."""
+    if V > INT_MAX or D > INT_MAX:
+        _fit("table", (V, D))
+    return V, D
 
 
 def embed_fwd(ids, table, scale: float = 1.0, lengths=None, dtype: Optional[torch.dtype] = None, out=None,
@@ -267,7 +290,7 @@ def embed_fwd(ids, table, scale: float = 1.0, lengths=None, dtype: Optional[torc
     _check(table, "table", device=dev)
     if table.dim() != 2:
         raise ValueError(f"table must be [V, D], got {tuple(table.shape)}")
-    V, D = table.shape
+    V, D = _table_sizes(*table.shape)
     table_code = _dtype_code(table)
     dt = dtype or (table.dtype if out is None else out.dtype)
     if dt not in (torch.bfloat16, torch.float32):
@@ -291,7 +314,7 @@ def embed_bwd(ids, d_out, V: int, scale: float = 1.0, lengths=None, d_table=None
     dev = _call_device(ids, stream)
     B, T, bits = _id_sizes(ids, lengths)
     _check(ids, "ids", device=dev)
-    D = d_out.shape[-1]
+    V, D = _table_sizes(V, d_out.shape[-1])
     code = _dtype_code(d_out)
     _check(d_out, "d_out", shape=tuple(ids.shape) + (D,), device=dev)
     _check(lengths, "lengths", torch.int32, required=False, shape=(B,), device=dev)
@@ -335,6 +358,13 @@ def _list_checks(tensors, name, dtype, params, dev, shapes=True):
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         raise ValueError(f"{name} must have the parameters' shapes, got {tuple(t.shape)} for {tuple(p.shape)}")
+
+
+def _step_number(step: int) -> int:
+    step = int(step)
+    if abs(step) > INT_MAX:
+        _fit("step", (abs(step),))
+    return step
 
 
 def _scalar(x, name, dtype, dev):
@@ -470,6 +500,6 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
         used = (*params, *grads, *exp_avg, *exp_avg_sq, *(exp_avg_scale or ()), *(exp_avg_sq_scale or ()),
                 *(copies or ()), *(x for x in (step, lr, grad_scale) if isinstance(x, torch.Tensor)))
     with _on(dev, stream, used):
-        _done(lib().prism_adamw_step(table, n, 0 if step_host is None else int(step_host), step_dev,
+        _done(lib().prism_adamw_step(table, n, 0 if step_host is None else _step_number(step_host), step_dev,
                                      0.0 if lr_host is None else float(lr_host), lr_dev, betas[0], betas[1], eps,
                                      grad_scale_dev, p_code, g_code, bits, _here(dev)), "prism_adamw_step")

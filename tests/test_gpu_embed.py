@@ -219,3 +219,12 @@ def test_refusals_name_the_argument():
     with pytest.raises(prism.PrismError, match="WORKSPACE"):
         prism.embed_bwd(ids, torch.zeros((2, 3, 8), device="cuda"), 4,
                         workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    # a table of 2^32 + 5 rows fits the device, and the C entry points take sizes of 32 bits
+    ids, d = torch.zeros((1, 3), dtype=torch.int64, device="cuda"), torch.ones((1, 3, 1), device="cuda")
+    with pytest.raises(prism.PrismError, match="UNSUPPORTED"):
+        prism.embed_bwd(ids, d, (1 << 32) + 5)
+    with pytest.raises(prism.PrismError, match="UNSUPPORTED"):
+        prism.embed_fwd(ids[:, :1].expand((1 << 32) + 5, 1), torch.zeros((1, 1), device="cuda"))

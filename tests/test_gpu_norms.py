@@ -443,3 +443,14 @@ def test_c_entry_points_take_gradients_in_place():
                                   ws.numel(), s) == 0
     assert torch.equal(dxo, want_b["x"]) and torch.equal(dyy, want_b["y"])
     assert all(torch.equal(a, want_b[n]) for a, n in zip(sums, ("weight", "post_weight", "scale")))
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    x, w = torch.zeros(1, 1, device="cuda").expand((1 << 32) + 8, 1), torch.ones(1, device="cuda")
+    with pytest.raises(prism.PrismError, match="UNSUPPORTED"):
+        prism.block_norm_fwd(x, w)
+    with pytest.raises(prism.PrismError, match="UNSUPPORTED"):
+        prism.block_norm_bwd(x, w, x)
+    o = torch.zeros(1, 1, 1, 16, device="cuda").expand(1, (1 << 32) + 8, 1, 16)
+    with pytest.raises(prism.PrismError, match="UNSUPPORTED"):
+        prism.gated_norm_fwd(o, None, torch.ones(16, device="cuda"))

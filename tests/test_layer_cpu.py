@@ -8,6 +8,7 @@ import torch
 
 import linear_attention_sequence_shortconv_b200 as prism
 from linear_attention_sequence_shortconv_b200 import build as prism_build
+from linear_attention_sequence_shortconv_b200 import layer_ops
 
 FAKE = [0x100000000 + (i << 32) for i in range(16)]  # aligned, far apart, never dereferenced
 INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
@@ -273,3 +274,22 @@ def test_dl_pointers():
     many = [_dl([257]), _dl([16, 16]), _dl([0, 3])]
     assert _gather(many, [_dl([2]), _dl([1]), _dl([0])], block=256)[0] == -1
     assert _gather(many, [_dl([1]), _dl([1]), _dl([0])], block=256)[0] == 3
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    # the C entry points take them as int: they must not arrive cut off
+    big = (1 << 32) + 5
+    meta = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype, device="meta")  # noqa: E731
+    for call in (lambda: layer_ops._heads(meta(big, 1, 1, 16)), lambda: layer_ops._heads(meta(1, big, 1, 16)),
+                 lambda: layer_ops._heads(meta(big, 1, 16)), lambda: layer_ops._stream_rows(meta(big, 1, 8)),
+                 lambda: layer_ops._stream_rows(meta(1, 1 << 31, 8)), lambda: layer_ops._stream_rows(meta(big, 1)),
+                 lambda: layer_ops._id_sizes(meta(big, dtype=torch.int64), None),
+                 lambda: layer_ops._id_sizes(meta(2, big, dtype=torch.int32), None),
+                 lambda: layer_ops._table_sizes(big, 1), lambda: layer_ops._table_sizes(1 << 31, 8),
+                 lambda: layer_ops._table_sizes(4, big), lambda: layer_ops._step_number(big),
+                 lambda: layer_ops._step_number(-big)):
+        with pytest.raises(prism.PrismError, match="UNSUPPORTED"):
+            call()
+    assert layer_ops._stream_rows(meta((1 << 31) - 1, 1)) == ((1 << 31) - 1, 1, 1)
+    assert layer_ops._id_sizes(meta(2, 3, dtype=torch.int32), None) == (2, 3, 32)
+    assert layer_ops._table_sizes(100, 8) == (100, 8) and layer_ops._step_number(7) == 7
