@@ -86,6 +86,7 @@ int check_block(int B, int T, int D, float res_scale, float eps, int x_dtype, in
   const int rc = check_tokens(B, T, D);
   if (rc != PRISM_OK) return rc;
   if (D > PRISM_MAX_WIDTH || (x_dtype == PRISM_BF16 && dtype == PRISM_FP32)) return PRISM_ERR_UNSUPPORTED;
+  if (D > 256 && (double)B * T > 2.0e9) return PRISM_ERR_UNSUPPORTED;  // the kernels number such rows in 32 bits
   return PRISM_OK;
 }
 

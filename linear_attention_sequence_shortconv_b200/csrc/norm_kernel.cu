@@ -24,6 +24,8 @@
 // bf16 61 us, 75%.  What was in the way before the memory: the instructions (half of what is
 // left are conversions, sums and exponentials, in packed pairs where the hardware has them),
 // and 32-byte sectors moved in two halves.
+#include <type_traits>
+
 #include "rowops.cuh"
 
 namespace prism {
@@ -66,6 +68,12 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return x;
 }
 
+template <int N>
+__device__ __forceinline__ void zero_pairs(float2 (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = both(0.f);
+}
+
 constexpr int kGnThreads = 256;
 
 // Where a thread's row stands, and whether it is to be read.  Index: 32 bits where every offset
@@ -104,13 +112,14 @@ __global__ void __launch_bounds__(kGnThreads) gated_norm_fwd_kernel(GatedNormPar
   struct {
     Raw8<T> o, g;
     Index row;
-    bool in;
+    bool in, valid;
   } r[ROWS];
 #pragma unroll
   for (int u = 0; u < ROWS; ++u) {
     const GatedAt<Index> at(p, ((Index)blockIdx.x * ROWS + u) * kPer + threadIdx.x / LPR, d);
     r[u].row = at.row;
     r[u].in = at.in;
+    r[u].valid = at.valid;
     if (at.valid) {
       r[u].o.template load<kWide>(static_cast<const T*>(p.o) + at.row * d, lane, LPR);
       if (GATE != kGateNone) r[u].g.template load<kWide>(static_cast<const T*>(p.gate) + at.gate, lane, LPR);
@@ -137,7 +146,7 @@ __global__ void __launch_bounds__(kGnThreads) gated_norm_fwd_kernel(GatedNormPar
         y[i] = mul2(y[i], GATE == kGateSilu ? mul2(g, sg) : sg);
       }
     }
-    // of padding, o is zero here and so is y (the gate was set to zero as well)
+    if (!r[u].valid) zero_pairs(y);  // a weight need not be finite
     store_shared8<kWide>(static_cast<T*>(p.y) + r[u].row * d, lane, LPR, d, y);
   }
 }
@@ -177,8 +186,9 @@ __global__ void __launch_bounds__(kGnThreads, 4) gated_norm_bwd_kernel(GatedNorm
   // the trip count is the same for the whole block
   for (Index base = (Index)blockIdx.x * kPer; base < rows; base += stride, row += stride, flags >>= 1) {
     ring.wait();
+    const bool valid = flags & 1;
     T *d_o_row = static_cast<T*>(p.y) + row * d, *dg_row = static_cast<T*>(p.d_gate) + row * d;
-    if (!__any_sync(0xffffffffu, flags & 1)) {  // a warp of padding
+    if (!__any_sync(0xffffffffu, valid)) {  // a warp of padding
       fetch(kStages - 1);
       ring.advance();
       const float2 zero[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
@@ -224,7 +234,11 @@ __global__ void __launch_bounds__(kGnThreads, 4) gated_norm_bwd_kernel(GatedNorm
       d_o[i] = mul2(fma2(xh, both(-mean), mul2(t[i], w[i])), both(r));
       if (GATE != kGateNone) dg[i] = mul2(dg[i], mul2(xh, w[i]));
     }
-    // padding was read as zero, and its gradients come out as zero
+    // padding was read as zero and adds nothing to dw; a weight need not be finite
+    if (!valid) {
+      zero_pairs(d_o);
+      if (GATE != kGateNone) zero_pairs(dg);
+    }
     store_shared8<kWide>(d_o_row, lane, LPR, d, d_o);
     if (GATE != kGateNone) store_shared8<kWide>(dg_row, lane, LPR, d, dg);
   }
@@ -311,6 +325,43 @@ __device__ __forceinline__ void store_row(T* p, int gt, int tpr, int D, const fl
       const float2 v[4] = {x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
       store_shared8<MAP == kEven4>(p + 8 * j * tpr, gt, tpr, D - 8 * j * tpr, v);
     }
+  }
+}
+
+// Padding.  A row of it was read as zeros, but the operations on zeros do not give zeros under a vector
+// that is not finite, nor leave the vectors' gradients alone.  With the ring and rows of whole warps
+// (columns per thread above 8, see BlockShape) a group goes from one row that is no padding to the
+// next, and sets its rows of padding to zero in the end.  Rows that share a warp go together, and
+// without the ring a branch before the row's use would part it from its loads (2991 x 1001 in fp32,
+// forward: 27 us instead of 15): there a row's results are replaced by zeros.
+template <int E, int MAP>
+__device__ constexpr bool pass_padding() { return E > 8 && MAP != kOdd; }
+
+// Number of a row: 32 bits for rows of more than 256 columns, of which no device holds 2^31.
+template <int E, int MAP>
+using RowIndex = typename std::conditional<pass_padding<E, MAP>(), uint32_t, long long>::type;
+
+// The first of the rows row, row + stride, ... that is no padding, or one behind the last.
+template <typename R>
+__device__ __forceinline__ R next_row(const BlockNormParams& p, R row, R stride) {
+  if (p.lengths)
+    while (row < (R)p.rows && !token_valid(row, p.T, p.lengths)) row += stride;
+  return row;
+}
+
+// Zeros into the rows of padding of this thread's group.  Last, and from the kernel's parameters alone:
+// the loop over the other rows has no register to spare for it.
+template <int E, int MAP, typename X, typename A>
+__device__ __forceinline__ void zero_padding(const BlockNormParams& p, bool x_out, bool h) {
+  if (!p.lengths) return;
+  using R = RowIndex<E, MAP>;
+  const int gt = threadIdx.x % p.tpr;
+  float2 x[E / 2];
+  zero_pairs(x);
+  for (R row = (R)blockIdx.x * p.groups + threadIdx.x / p.tpr; row < (R)p.rows; row += (R)gridDim.x * p.groups) {
+    if (token_valid(row, p.T, p.lengths)) continue;
+    if (x_out) store_row<E, MAP>(static_cast<X*>(p.x_out) + (long long)row * p.D, gt, p.tpr, p.D, x);
+    if (h) store_row<E, MAP>(static_cast<A*>(p.h) + (long long)row * p.D, gt, p.tpr, p.D, x);
   }
 }
 
@@ -420,9 +471,10 @@ struct BwdRows {
   const BlockNormParams& p;
   int gt;
   Ring<kAll, kBnStages> ring;
+  bool valid, next_valid;  // whether the row at hand, and the one behind it, exist and are no padding
   __device__ __forceinline__ BwdRows(const BlockNormParams& p_, int gt_, void* smem) : p(p_), gt(gt_), ring(smem) {}
   __device__ __forceinline__ void fetch(int ahead, long long row) {
-    const bool ok = row < p.rows && token_valid(row, p.T, p.lengths);
+    const bool ok = next_valid = row < p.rows && (pass_padding<E, MAP>() || token_valid(row, p.T, p.lengths));
     copy_row<MAP, X, E>(ring, ahead, 0, p.x, row, p, gt, ok);
     copy_row<MAP, X, E>(ring, ahead, kX, p.dx_in ? p.dx_in : p.x, row, p, gt, ok && p.dx_in);
     copy_row<MAP, A, E>(ring, ahead, 2 * kX, p.dh, row, p, gt, ok);
@@ -433,6 +485,7 @@ struct BwdRows {
   // the row's set is complete; the one behind it, which the previous row has been through, is filled
   __device__ __forceinline__ void take(long long, long long next) {
     ring.wait();
+    valid = next_valid;
     fetch(1, next);
   }
   __device__ __forceinline__ void leave() { ring.advance(); }
@@ -451,10 +504,11 @@ struct BwdRows<X, A, E, kOdd, Y> {
   int gt;
   Row<X, E> rx, rdx;
   Row<A, E> rdh, ry;
+  bool valid;
   __device__ __forceinline__ BwdRows(const BlockNormParams& p_, int gt_, void*) : p(p_), gt(gt_) {}
   __device__ __forceinline__ void start(long long) {}
   __device__ __forceinline__ void take(long long row, long long) {
-    const bool ok = row < p.rows && token_valid(row, p.T, p.lengths);
+    const bool ok = valid = row < p.rows && token_valid(row, p.T, p.lengths);
     rx.load(static_cast<const X*>(p.x) + row * p.D, gt, p.tpr, p.D, ok);
     rdh.load(static_cast<const A*>(p.dh) + row * p.D, gt, p.tpr, p.D, ok);
     rdx.load(static_cast<const X*>(p.dx_in) + row * p.D, gt, p.tpr, p.D, ok && p.dx_in);
@@ -475,9 +529,10 @@ struct FwdRows {
   const BlockNormParams& p;
   int gt;
   Ring<kAll, kBnStages> ring;
+  bool valid, next_valid;
   __device__ __forceinline__ FwdRows(const BlockNormParams& p_, int gt_, void* smem) : p(p_), gt(gt_), ring(smem) {}
   __device__ __forceinline__ void fetch(int ahead, long long row) {
-    const bool ok = row < p.rows && token_valid(row, p.T, p.lengths);
+    const bool ok = next_valid = row < p.rows && (pass_padding<E, MAP>() || token_valid(row, p.T, p.lengths));
     copy_row<MAP, X, E>(ring, ahead, 0, p.x, row, p, gt, ok);
     if (DELTA) copy_row<MAP, A, E>(ring, ahead, kX, p.y, row, p, gt, ok);
     ring.commit();
@@ -485,6 +540,7 @@ struct FwdRows {
   __device__ __forceinline__ void start(long long row) { fetch(0, row); }
   __device__ __forceinline__ void take(long long, long long next) {
     ring.wait();
+    valid = next_valid;
     fetch(1, next);
   }
   __device__ __forceinline__ void leave() { ring.advance(); }
@@ -500,10 +556,11 @@ struct FwdRows<X, A, E, kOdd, DELTA> {
   int gt;
   Row<X, E> rx;
   Row<A, E> ry;
+  bool valid;
   __device__ __forceinline__ FwdRows(const BlockNormParams& p_, int gt_, void*) : p(p_), gt(gt_) {}
   __device__ __forceinline__ void start(long long) {}
   __device__ __forceinline__ void take(long long row, long long) {
-    const bool ok = row < p.rows && token_valid(row, p.T, p.lengths);
+    const bool ok = valid = row < p.rows && token_valid(row, p.T, p.lengths);
     rx.load(static_cast<const X*>(p.x) + row * p.D, gt, p.tpr, p.D, ok);
     if (DELTA) ry.load(static_cast<const A*>(p.y) + row * p.D, gt, p.tpr, p.D, ok);
   }
@@ -526,17 +583,21 @@ __global__ void __launch_bounds__(fwd_threads(E), fwd_blocks(E)) block_norm_fwd_
   const int tpr = p.tpr, gt = threadIdx.x % tpr, group = threadIdx.x / tpr, D = p.D, n = tpr * E;
   GroupSum sum{buf};
   FwdRows<X, A, E, MAP, DELTA> rows(p, gt, vecs + (1 + DELTA + POST) * n);
-  const long long stride = (long long)gridDim.x * p.groups;
-  long long row = (long long)blockIdx.x * p.groups + group;
+  constexpr bool kPass = pass_padding<E, MAP>();
+  using R = RowIndex<E, MAP>;
+  const R stride = (R)gridDim.x * p.groups, end = (R)p.rows;
+  R row = (R)blockIdx.x * p.groups + group, next;
+  if (kPass) row = next_row(p, row, stride);
   rows.start(row);
   stage_vec<MAP>(vecs, p.weight, D, n, tpr, 1.f, 1.f);
   if (DELTA) stage_vec<MAP>(vecs + n, p.scale, D, n, tpr, 1.f, p.res_scale);
   if (POST) stage_vec<MAP>(vecs + 2 * n, p.post_weight, D, n, tpr, 1.f, 1.f);
   __syncthreads();
-  // the trip count is the same for the whole block, which groups of several warps need
-  for (long long base = (long long)blockIdx.x * p.groups; base < p.rows; base += stride, row += stride) {
-    rows.take(row, row + stride);
-    const bool in = row < p.rows;
+  // rows that share a warp: the trip count is the same for the whole block
+  for (R base = row - group; (kPass ? row : base) < end; base += stride, row = next) {
+    next = kPass ? next_row<R>(p, row + stride, stride) : row + stride;
+    rows.take(row, next);
+    const bool in = kPass || row < end, valid = kPass || rows.valid;
     float2 x[P], q = both(0.f);
     float s[1], ry = 1.f;
     if (POST) {
@@ -568,7 +629,8 @@ __global__ void __launch_bounds__(fwd_threads(E), fwd_blocks(E)) block_norm_fwd_
         q = fma2(v, v, q);
       }
     }
-    if (DELTA && in) store_row<E, MAP>(static_cast<X*>(p.x_out) + row * D, gt, tpr, D, x);
+    if (!valid) zero_pairs(x);
+    if (DELTA && in) store_row<E, MAP>(static_cast<X*>(p.x_out) + (long long)row * D, gt, tpr, D, x);
     s[0] = q.x + q.y;
     sum.run(s, group, gt, tpr);
     const float r = rsqrtf(s[0] * p.inv_D + p.eps);
@@ -578,10 +640,12 @@ __global__ void __launch_bounds__(fwd_threads(E), fwd_blocks(E)) block_norm_fwd_
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[4 * j + i] = mul2(mul2(x[4 * j + i], both(r)), w.v[i]);
     }
-    if (in) store_row<E, MAP>(static_cast<A*>(p.h) + row * D, gt, tpr, D, x);
+    if (!valid) zero_pairs(x);
+    if (in) store_row<E, MAP>(static_cast<A*>(p.h) + (long long)row * D, gt, tpr, D, x);
     rows.leave();
   }
   rows.finish();
+  if (kPass) zero_padding<E, MAP, X, A>(p, DELTA, true);
 }
 
 // Most threads of a block of the backward.  One block fills an SM: fewer blocks leave fewer
@@ -605,8 +669,11 @@ __global__ void __launch_bounds__(bwd_threads(E, MAP != kOdd), 1)
   GroupSum sum{buf};
   BwdRows<X, A, E, MAP, Y> rows(p, gt, vecs + max(3, p.groups) * n);
   launch_dependents();
-  const long long stride = (long long)gridDim.x * p.groups;
-  long long row = (long long)blockIdx.x * p.groups + group;
+  constexpr bool kPass = pass_padding<E, MAP>();
+  using R = RowIndex<E, MAP>;
+  const R stride = (R)gridDim.x * p.groups, end = (R)p.rows;
+  R row = (R)blockIdx.x * p.groups + group, next;
+  if (kPass) row = next_row(p, row, stride);
   rows.start(row);
   stage_vec<MAP>(vecs, p.weight, D, n, tpr, 1.f, 1.f);
   if (DELTA) stage_vec<MAP>(vecs + n, p.scale, D, n, tpr, 1.f, p.res_scale);
@@ -615,10 +682,11 @@ __global__ void __launch_bounds__(bwd_threads(E, MAP != kOdd), 1)
   float2 aw[P], ap[P], as[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) aw[i] = ap[i] = as[i] = both(0.f);
-  // the trip count is the same for the whole block, which groups of several warps need
-  for (long long base = (long long)blockIdx.x * p.groups; base < p.rows; base += stride, row += stride) {
-    rows.take(row, row + stride);
-    const bool in = row < p.rows;
+  // rows that share a warp: the trip count is the same for the whole block
+  for (; (kPass ? row : row - group) < end; row = next) {
+    next = kPass ? next_row<R>(p, row + stride, stride) : row + stride;
+    rows.take(row, next);
+    const bool in = kPass || row < end, valid = kPass || rows.valid;
     float s[N];
     float2 q0 = both(0.f), q1 = both(0.f), q2 = both(0.f);
 #pragma unroll
@@ -652,26 +720,29 @@ __global__ void __launch_bounds__(bwd_threads(E, MAP != kOdd), 1)
         dx[4 * j + i] = fma2(fma2(xh, both(-mean), mul2(dh.v[i], w.v[i])), both(r), d.v[i]);
       }
     }
-    if (in) store_row<E, MAP>(static_cast<X*>(p.x_out) + row * D, gt, tpr, D, dx);
+    if (!valid) zero_pairs(dx);
+    if (in) store_row<E, MAP>(static_cast<X*>(p.x_out) + (long long)row * D, gt, tpr, D, dx);
     if (DELTA) {
+      if (valid) {
 #pragma unroll
-      for (int j = 0; j < E / 8; ++j) {
-        const Piece k = vec_piece<MAP>(vecs + n, j, gt, tpr);
-        Piece y, wp;
-        if (Y) y = rows.y(j);
-        if (POST) wp = vec_piece<MAP>(vecs + 2 * n, j, gt, tpr);
+        for (int j = 0; j < E / 8; ++j) {
+          const Piece k = vec_piece<MAP>(vecs + n, j, gt, tpr);
+          Piece y, wp;
+          if (Y) y = rows.y(j);
+          if (POST) wp = vec_piece<MAP>(vecs + 2 * n, j, gt, tpr);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float2& d = dx[4 * j + i];
-          if (POST) {
-            const float2 yh = mul2(y.v[i], both(ry)), dz = mul2(d, k.v[i]);
-            if (SCALE) as[4 * j + i] = fma2(d, mul2(yh, wp.v[i]), as[4 * j + i]);  // times res_scale at the end
-            ap[4 * j + i] = fma2(dz, yh, ap[4 * j + i]);
-            d = mul2(dz, wp.v[i]);
-            c2 = fma2(d, yh, c2);
-          } else {
-            if (SCALE) as[4 * j + i] = fma2(d, y.v[i], as[4 * j + i]);
-            d = mul2(d, k.v[i]);
+          for (int i = 0; i < 4; ++i) {
+            float2& d = dx[4 * j + i];
+            if (POST) {
+              const float2 yh = mul2(y.v[i], both(ry)), dz = mul2(d, k.v[i]);
+              if (SCALE) as[4 * j + i] = fma2(d, mul2(yh, wp.v[i]), as[4 * j + i]);  // times res_scale at the end
+              ap[4 * j + i] = fma2(dz, yh, ap[4 * j + i]);
+              d = mul2(dz, wp.v[i]);
+              c2 = fma2(d, yh, c2);
+            } else {
+              if (SCALE) as[4 * j + i] = fma2(d, y.v[i], as[4 * j + i]);
+              d = mul2(d, k.v[i]);
+            }
           }
         }
       }
@@ -686,7 +757,7 @@ __global__ void __launch_bounds__(bwd_threads(E, MAP != kOdd), 1)
           for (int i = 0; i < 4; ++i) dx[4 * j + i] = mul2(fma2(y.v[i], both(my), dx[4 * j + i]), both(ry));
         }
       }
-      if (in) store_row<E, MAP>(static_cast<A*>(p.h) + row * D, gt, tpr, D, dx);
+      if (in) store_row<E, MAP>(static_cast<A*>(p.h) + (long long)row * D, gt, tpr, D, dx);
     }
     rows.leave();
   }
@@ -709,6 +780,7 @@ __global__ void __launch_bounds__(bwd_threads(E, MAP != kOdd), 1)
       out[c] = t;
     }
   }
+  if (kPass) zero_padding<E, MAP, X, A>(p, true, DELTA);
 }
 
 // Eight columns (one 32-byte sector of a row) and 64 slices of the rows per block.
@@ -811,7 +883,7 @@ struct BlockShape {
     if (bwd) E = D <= 1024 && vec ? (D + 255) / 256 * 8 : vec ? 16 : D <= 4096 ? 8 : 16;
     else E = D <= 1024 ? (D + 255) / 256 * 8 : 16;
     const int t = (D + E - 1) / E, most = bwd ? bwd_threads(E, vec) : fwd_threads(E);
-    tpr = 1;
+    tpr = E > 8 ? 32 : 1;  // pass_padding()
     while (tpr < 32 && tpr < t) tpr *= 2;
     if (t > 32) tpr = (t + 31) / 32 * 32;
     groups = most / tpr;

@@ -454,3 +454,73 @@ def test_sizes_beyond_32_bits_are_refused():
     o = torch.zeros(1, 1, 1, 16, device="cuda").expand(1, (1 << 32) + 8, 1, 16)
     with pytest.raises(prism.PrismError, match="UNSUPPORTED"):
         prism.gated_norm_fwd(o, None, torch.ones(16, device="cuda"))
+
+
+# ------------------------------------------------------------- padding under weights that are not finite
+BAD = [float("inf"), float("nan")]
+
+
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("d,dtype,gate", [(16, "bf16", "dense"), (32, "fp32", "none"), (64, "bf16", "none"),
+                                          (64, "fp32", "dense"), (128, "bf16", "slice"), (128, "fp32", "dense")])
+def test_gated_norm_padding_is_zero_whatever_the_weight(bad, d, dtype, gate):
+    B, T, H = 3, 37, 5
+    o, g, w, dy = _gated_inputs(B, T, H, d, DT[dtype], gate)
+    gc = None if g is None else torch.empty_strided(g.shape, g.stride(), dtype=g.dtype, device="cuda").copy_(g)
+    w[3] = bad
+    for lengths in ([T, 0, 11], [0, 0, 0]):
+        lens = torch.tensor(lengths, dtype=torch.int32).cuda()
+        y = prism.gated_norm_fwd(o.cuda(), gc, w.cuda(), lengths=lens)
+        got = prism.gated_norm_bwd(o.cuda(), gc, w.cuda(), dy.cuda(), lengths=lens)
+        pad = ~ref.valid_rows(lengths, B, T)
+        for t in (y, got["o"], got["gate"]):
+            assert t is None or t.cpu()[pad].eq(0).all()
+        assert any(lengths) or got["weight"].eq(0).all()
+        # a valid row is what it was: not finite where the weight is not
+        assert not any(lengths) or not torch.isfinite(y[0, :, :, 3]).any()
+
+
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("which", ["weight", "post_weight", "scale"])
+@pytest.mark.parametrize("D,stream,dtype,post,scale", [
+    (8, "bf16", "bf16", True, True), (40, "fp32", "bf16", True, True), (77, "bf16", "bf16", True, True),
+    (77, "fp32", "fp32", False, True), (768, "bf16", "bf16", True, True), (768, "fp32", "bf16", True, False),
+    (1001, "fp32", "fp32", True, True), (2056, "bf16", "bf16", True, True), (2056, "fp32", "bf16", False, True),
+    (4099, "bf16", "bf16", True, True)])
+def test_block_norm_padding_is_zero_whatever_the_vectors(bad, which, D, stream, dtype, post, scale):
+    B, T = 3, 37
+    x, w, vec, dh, dxo = _block_inputs(B, T, D, stream, dtype, True, post, scale)
+    vec["weight"] = w
+    if vec[which] is None:
+        pytest.skip("the vector is not given")
+    vec[which][3] = bad
+    w = vec.pop("weight").cuda()
+    v = {n: _cuda(t) for n, t in vec.items()}
+    for lengths in ([T, 0, 11], [0, 0, 0]):
+        lens = torch.tensor(lengths, dtype=torch.int32).cuda()
+        pad = ~ref.valid_rows(lengths, B, T)
+        outs = list(prism.block_norm_fwd(x.cuda(), w, lengths=lens, **v))
+        got = prism.block_norm_bwd(x.cuda(), w, dh.cuda(), dx_out=dxo.cuda(), lengths=lens, **v)
+        outs += [got["x"], got["y"]]
+        if which == "weight":  # without y there is only h
+            outs += [prism.block_norm_fwd(x.cuda(), w, lengths=lens)[1],
+                     prism.block_norm_bwd(x.cuda(), w, dh.cuda(), lengths=lens)["x"]]
+        for t in outs:
+            assert t.cpu()[pad].eq(0).all()
+        if not any(lengths):  # padding adds nothing to any vector's gradient
+            assert all(got[n].eq(0).all() for n in ("weight", "post_weight", "scale") if got[n] is not None)
+
+
+def test_places_behind_the_last_row_add_nothing_to_the_vectors_gradients():
+    # fewer rows than a block has places for, and an infinite scale: the sum of infinities of one sign
+    # over the rows is that infinity, and becomes NaN if a place without a row adds 0 * inf
+    D = 40
+    x, w, vec, dh, dxo = _block_inputs(1, 5, D, "fp32", "fp32", True, True, True)
+    v = {n: t.cuda() for n, t in vec.items()}
+    dx = prism.block_norm_bwd(x.cuda(), w.cuda(), dh.cuda(), dx_out=dxo.cuda(), **v)["x"]  # depends on neither
+    v["y"][..., 3] = torch.where(dx[..., 3] > 0, 0.5, -0.5)
+    want = prism.block_norm_bwd(x.cuda(), w.cuda(), dh.cuda(), dx_out=dxo.cuda(), **v)
+    v["scale"][3] = float("inf")
+    got = prism.block_norm_bwd(x.cuda(), w.cuda(), dh.cuda(), dx_out=dxo.cuda(), **v)
+    want["post_weight"][3] = float("inf")
+    assert all(torch.equal(got[n], want[n]) for n in ("x", "weight", "scale", "post_weight"))
