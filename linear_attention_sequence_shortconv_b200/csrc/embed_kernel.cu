@@ -22,7 +22,7 @@
 // before: with rows of 8 elements, where there is nothing to move, 32768 tokens take 33 us (sort
 // 13.5, sums 14, joins 8, less what the chained launches overlap).  Measured: 130M LM, 32768
 // tokens, dense gradient of 32000 x 768: 56 us (floor 22.7); recommendation batch, added to
-// 1000003 x 128: 49 us (floor 11); a million tokens over two rows of 64: 71 us (without the
+// 1000003 x 128: 51 us (floor 11); a million tokens over two rows of 64: 71 us (without the
 // fold 1154), over 3000: 118 us (searching the sorted keys for rows without a token: 205).
 #include <cooperative_groups.h>
 
@@ -451,27 +451,17 @@ struct Columns {
         if (first + e * step < D) row[first + e * step] = x[e];
     }
   }
-  // The finished sum of table row v.  Adding to what the row holds takes the memory's own add, so
-  // that nobody waits for the old values; each element gets one addition in all (a row is finished
-  // once), so the order of execution does not show.  That add treats subnormal numbers as zero.
+  // The finished sum of table row v, which is finished once: nobody else reads or writes the row.
+  // (Adding by the memory's own add, which nobody waits for, is 4% faster but treats what the row
+  // holds below 2^-126 as zero.)
   __device__ __forceinline__ void finish(const EmbedParams& p, uint32_t v, const float (&x)[8]) const {
     float* row = p.d_table + (size_t)v * D;
     float y[8];
+    if (p.accumulate) load(row, y);
+    else zero8(y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = p.scale * x[e];
-    if (!p.accumulate) return store(row, y);
-    if (VEC) {
-      if (first >= D) return;
-#pragma unroll
-      for (int e = 0; e < 8; e += 4)
-        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(row + first + e), "f"(y[e]), "f"(y[e + 1]),
-                     "f"(y[e + 2]), "f"(y[e + 3]) : "memory");
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (first + e * step < D)
-          asm volatile("red.global.add.f32 [%0], %1;" ::"l"(row + first + e * step), "f"(y[e]) : "memory");
-    }
+    for (int e = 0; e < 8; ++e) y[e] += p.scale * x[e];
+    store(row, y);
   }
 };
 

@@ -228,3 +228,20 @@ def test_sizes_beyond_32_bits_are_refused():
         prism.embed_bwd(ids, d, (1 << 32) + 5)
     with pytest.raises(prism.PrismError, match="UNSUPPORTED"):
         prism.embed_fwd(ids[:, :1].expand((1 << 32) + 5, 1), torch.zeros((1, 1), device="cuda"))
+
+
+@pytest.mark.parametrize("D", [8, 9, 64])
+@pytest.mark.parametrize("kind", ["even", "one", "runs"])
+def test_subnormal_numbers_are_added_to_and_kept(D, kind):
+    # what a named row holds below 2^-126 stays, and so does a sum down there.  All values are
+    # multiples of 2^-149 below 2^-126, so that every sum is exact in any order
+    V, N = 300, 1500
+    ids = _ids(1, N, V, 64, kind)
+    tiny = 2.0 ** -149
+    old = (torch.randint(-4000, 4000, (V, D), generator=_gen(1)).double() * tiny).float()
+    d = (torch.randint(-1000, 1000, (1, N, D), generator=_gen(2)).double() * tiny).float()
+    want = old.double().index_add_(0, ids.view(-1), d.double().view(-1, D))
+    got = prism.embed_bwd(ids.cuda(), d.cuda(), V, d_table=old.cuda(), accumulate=True)
+    assert torch.equal(got.double().cpu(), want)
+    dense = prism.embed_bwd(ids.cuda(), d.cuda(), V)
+    assert torch.equal(dense.double().cpu(), want - old.double())
