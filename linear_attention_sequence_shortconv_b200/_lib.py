@@ -12,6 +12,7 @@ import os
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.graph import increment_version
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # PRISM_DEBUG_BOUNDS=1 in the environment loads the debug build (bounds-checked kernels)
@@ -215,6 +216,12 @@ def _check(t: Optional[torch.Tensor], name: str, dtype=None, required=True, shap
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _wrote(*tensors: Optional[torch.Tensor]) -> None:
+    """Tells autograd that a call has written to tensors that the caller gave: a graph that still
+    needs their old values then fails instead of taking the new ones."""
+    increment_version([t for t in tensors if t is not None])
+
+
 def _call_device(first: torch.Tensor, stream) -> torch.device:
     """The device a call runs on: that of its first tensor argument.  The library launches
     on the current CUDA device, so every entry point below runs inside
@@ -286,6 +293,7 @@ def scan_fwd(q, k, v, gamma, beta, u, alpha, gain, conv_w, L: int, chunk: int = 
     Every tensor must be on one CUDA device; the call runs on that device.
     """
     chain_code = _chain_code(chain)
+    given = (o, S_final if want_state else None)
     (B, T, H, d_k, d_v, W, code), dev, o, S_final = _scan_checks(
         q, k, v, gamma, beta, u, alpha, gain, conv_w, L, S0, lengths, o, S_final, want_state, stream, conv_state)
     with torch.cuda.device(dev):
@@ -304,6 +312,7 @@ def scan_fwd(q, k, v, gamma, beta, u, alpha, gain, conv_w, L: int, chunk: int = 
             chain_code, _ptr(conv_state if W > 1 else None))
     if rc != 0:
         raise PrismError(rc, "prism_scan_fwd_ex")
+    _wrote(*given)
     return o, (S_final if want_state else None)
 
 
@@ -313,6 +322,7 @@ def scan_fwd_static(q, k, v, gamma, beta, u, alpha, gain, conv_w, L: int, chunk:
     """scan_fwd through prism_scan_fwd_static: no workspace argument, and the library
     allocates nothing (its scratch is a device-global array); returns (o, S_final)."""
     chain_code = _chain_code(chain)
+    given = (o, S_final if want_state else None)
     (B, T, H, d_k, d_v, W, code), dev, o, S_final = _scan_checks(
         q, k, v, gamma, beta, u, alpha, gain, conv_w, L, S0, lengths, o, S_final, want_state, stream, conv_state)
     with torch.cuda.device(dev):
@@ -325,6 +335,7 @@ def scan_fwd_static(q, k, v, gamma, beta, u, alpha, gain, conv_w, L: int, chunk:
             _ptr(conv_state if W > 1 else None))
     if rc != 0:
         raise PrismError(rc, "prism_scan_fwd_static")
+    _wrote(*given)
     return o, (S_final if want_state else None)
 
 
@@ -362,6 +373,7 @@ def scan_fwd_host(host: dict, dev: dict, L: int, chunk: int = 64, stream=None):
             _ptr(ws), ws.numel() if ws is not None else 0, _stream_handle(stream))
     if rc != 0:
         raise PrismError(rc, "prism_scan_fwd_host")
+    _wrote(host["o"], host.get("S_final"), *(dev.get(n) for n in names + ("o", "S_final")))
 
 
 def prologue_fwd(v, alpha, gain, conv_w, L: int, lengths=None, stream=None, chain: str = "linear"):
@@ -414,6 +426,7 @@ def decode_step(q, k, v, gamma, beta, u, alpha, gain, conv_w, conv_state, S, L: 
         _check(gain, "gain", dt, shape=(B, H, m, d_v), device=dev)
         _check(alpha, "alpha", torch.float32, shape=(B, H, m), device=dev)
     _check(conv_state, "conv_state", dt, required=W > 1, shape=(B, H, W - 1, d_v), device=dev)
+    written = (o, S, conv_state if W > 1 else None)
     if o is None:
         o = torch.empty((B, H, d_v), dtype=dt, device=dev)
     else:
@@ -426,6 +439,7 @@ def decode_step(q, k, v, gamma, beta, u, alpha, gain, conv_w, conv_state, S, L: 
             B, H, d_k, d_v, L, W, code, chain_code, _ptr(o), _stream_handle(stream))
     if rc != 0:
         raise PrismError(rc, "prism_decode_step")
+    _wrote(*written)
     return o
 
 
@@ -442,6 +456,7 @@ def state_affine(S, M, N=None, out=None, stream=None):
         raise ValueError(f"M must be {tuple(S.shape[:-2]) + (d_k, d_k)}, got {tuple(M.shape)}")
     if N is not None and tuple(N.shape) != tuple(S.shape):
         raise ValueError(f"N must be {tuple(S.shape)}, got {tuple(N.shape)}")
+    given = out
     if out is None:
         out = torch.empty_like(S)
     else:
@@ -451,6 +466,7 @@ def state_affine(S, M, N=None, out=None, stream=None):
         rc = lib().prism_state_affine(_ptr(S), _ptr(M), _ptr(N), _ptr(out), BH, d_v, d_k, _stream_handle(stream))
     if rc != 0:
         raise PrismError(rc, "prism_state_affine")
+    _wrote(given)
     return out
 
 

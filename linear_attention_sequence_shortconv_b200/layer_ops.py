@@ -3,7 +3,8 @@ norm of its readout, the norm at the border of a residual block, the embedding a
 step.  As in the mixer's binding, every step runs in the library's CUDA kernels; there is no
 CPU path, and a call runs on the device of its tensors, on torch's current stream or on
 ``stream``.  With ``stream`` given, what the call allocates belongs to that stream, and the
-caller orders the stream behind the work that made the inputs.
+caller orders the stream behind the work that made the inputs.  Tensors of the caller that a call
+writes get a new version, so that an autograd graph that needs their old values fails.
 """
 from __future__ import annotations
 
@@ -15,8 +16,9 @@ import itertools
 from typing import Dict, List, Optional, Sequence, Union
 
 import torch
+from torch.autograd.graph import increment_version
 
-from ._lib import LIB_PATH, PRISM_BF16, PRISM_FP32, PrismError, _call_device, _dtype_code, lib
+from ._lib import LIB_PATH, PRISM_BF16, PRISM_FP32, PrismError, _call_device, _dtype_code, _wrote, lib
 from ._lib import _check as _check_slow
 
 PRISM_ACT_SILU = 0
@@ -142,11 +144,14 @@ def gated_norm_fwd(o, gate, weight, lengths=None, eps: float = 1e-5, act: str = 
     _check(weight, "weight", torch.float32, shape=(d,), device=dev)
     _check(lengths, "lengths", torch.int32, required=False, shape=(B,), device=dev)
     _check(y, "y", o.dtype, required=False, shape=o.shape, device=dev)
+    given = y
     with _on(dev, stream, (o, gate, weight, lengths, y)):
         if y is None:
             y = torch.empty_like(o)
         _done(lib().prism_gated_norm_fwd(_ptr(o), _ptr(gate), _ptr(weight), _ptr(lengths), B, T, H, d, stride, eps,
                                          act_code, code, _ptr(y), _here(dev)), "prism_gated_norm_fwd")
+    if given is not None:
+        _wrote(given)
     return y
 
 
@@ -220,6 +225,7 @@ def block_norm_fwd(x, weight, y=None, post_weight=None, scale=None, res_scale: f
     code = PRISM_BF16 if dt == torch.bfloat16 else PRISM_FP32
     _check(x_out, "x_out", x.dtype, required=False, shape=x.shape, device=dev)
     _check(h, "h", dt, required=False, shape=x.shape, device=dev)
+    given = (None if y is None else x_out, h)
     with _on(dev, stream, (x, weight, y, post_weight, scale, lengths, x_out, h)):
         if y is None:
             x_out = x
@@ -231,6 +237,8 @@ def block_norm_fwd(x, weight, y=None, post_weight=None, scale=None, res_scale: f
                                          _ptr(lengths), B, T, D, res_scale, eps, x_code, code,
                                          _ptr(x_out if y is not None else None), _ptr(h), _here(dev)),
               "prism_block_norm_fwd")
+    if any(t is not None for t in given):
+        _wrote(*given)
     return x_out, h
 
 
@@ -297,12 +305,15 @@ def embed_fwd(ids, table, scale: float = 1.0, lengths=None, dtype: Optional[torc
         raise TypeError(f"dtype must be bfloat16 or float32, got {dt}")
     _check(lengths, "lengths", torch.int32, required=False, shape=(B,), device=dev)
     _check(out, "out", dt, required=False, shape=tuple(ids.shape) + (D,), device=dev)
+    given = out
     with _on(dev, stream, (ids, table, lengths, out)):
         if out is None:
             out = torch.empty(tuple(ids.shape) + (D,), dtype=dt, device=dev)
         _done(lib().prism_embed_fwd(_ptr(ids), _ptr(table), _ptr(lengths), B, T, V, D, scale, bits, table_code,
                                     PRISM_BF16 if dt == torch.bfloat16 else PRISM_FP32, _ptr(out), _here(dev)),
               "prism_embed_fwd")
+    if given is not None:
+        _wrote(given)
     return out
 
 
@@ -319,6 +330,7 @@ def embed_bwd(ids, d_out, V: int, scale: float = 1.0, lengths=None, d_table=None
     _check(d_out, "d_out", shape=tuple(ids.shape) + (D,), device=dev)
     _check(lengths, "lengths", torch.int32, required=False, shape=(B,), device=dev)
     _check(d_table, "d_table", torch.float32, required=accumulate, shape=(V, D), device=dev)
+    given = d_table
     with _on(dev, stream, (ids, d_out, lengths, d_table, workspace)):
         if d_table is None:
             d_table = torch.empty((V, D), dtype=torch.float32, device=dev)
@@ -326,6 +338,8 @@ def embed_bwd(ids, d_out, V: int, scale: float = 1.0, lengths=None, d_table=None
         _done(lib().prism_embed_bwd(_ptr(ids), _ptr(d_out), _ptr(lengths), B, T, V, D, scale, bits, code,
                                     int(accumulate), _ptr(d_table), _ptr(workspace), workspace.numel(), _here(dev)),
               "prism_embed_bwd")
+    if given is not None:
+        _wrote(given)
     return d_table
 
 
@@ -503,3 +517,5 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
         _done(lib().prism_adamw_step(table, n, 0 if step_host is None else _step_number(step_host), step_dev,
                                      0.0 if lr_host is None else float(lr_host), lr_dev, betas[0], betas[1], eps,
                                      grad_scale_dev, p_code, g_code, bits, _here(dev)), "prism_adamw_step")
+    increment_version([*params, *exp_avg, *exp_avg_sq, *(exp_avg_scale or ()), *(exp_avg_sq_scale or ()),
+                       *(copies or ())])

@@ -218,3 +218,51 @@ def test_training_step_replayed_from_a_graph():
         runs.append([p[n] for n in names] + [t.float() for x in state.values() for t in x])
     assert prism.stream_status() == 0
     assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+def test_autograd_sees_what_a_call_writes():
+    # a graph that still needs the old values fails instead of taking the new ones
+    r = lambda *s: torch.randn(s, device="cuda")  # noqa: E731
+    w = torch.nn.Parameter(r(300))
+    for bits in (32, 8):
+        state = prism.adamw_state([w], bits=bits)
+        loss = (w * w).sum()
+        with torch.no_grad():
+            prism.adamw_step([w], [r(300)], **state)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+
+    def bumps(written, call):
+        before = [t._version for t in written]
+        call()
+        assert all(t._version > v for t, v in zip(written, before))
+
+    p, g = [r(300)], [r(300)]
+    for bits in (32, 8):
+        state, copies = prism.adamw_state(p, bits=bits), [torch.zeros(300, dtype=torch.bfloat16, device="cuda")]
+        bumps([*p, *copies, *(t for x in state.values() for t in x)],
+              lambda: prism.adamw_step(p, g, copies=copies, **state))
+    assert g[0]._version == 0
+    o, x, y, h, out, dt = r(2, 3, H, d), r(2, 3, D), r(2, 3, D), r(2, 3, D), r(2, 3, D), r(V, D)
+    ids = torch.zeros((2, 3), dtype=torch.int64, device="cuda")
+    bumps([o], lambda: prism.gated_norm_fwd(o, None, r(d), y=o))
+    bumps([x, h], lambda: prism.block_norm_fwd(x, r(D), y=y, x_out=x, h=h))
+    bumps([h], lambda: prism.block_norm_fwd(x, r(D), h=h))
+    bumps([out], lambda: prism.embed_fwd(ids, dt, out=out))
+    bumps([dt], lambda: prism.embed_bwd(ids, out, V, d_table=dt, accumulate=True))
+    assert y._version == 0 and ids._version == 0
+    # the mixer's calls as well
+    S, hist, ob = r(2, H, d, d), r(2, H, W - 1, d), r(2, H, d)
+    q, gamma = r(2, H, d), torch.rand((2, H), device="cuda")
+    bumps([S, hist, ob], lambda: prism.decode_step(q, q, q, gamma, gamma, None, None, None, r(H, d, W), hist, S, L=1,
+                                                   o=ob))
+    q, gamma, os = r(2, 3, H, d), torch.rand((2, 3, H), device="cuda"), r(2, 3, H, d)
+    for scan in (prism.scan_fwd, prism.scan_fwd_static):
+        bumps([S, os], lambda: scan(q, q, q, gamma, gamma, None, None, None, r(H, d, W), L=1, chunk=16, o=os, S_final=S))
+    bumps([S], lambda: prism.state_affine(S, r(2, H, d, d), out=S))
+    assert q._version == 0 and gamma._version == 0
+    # inference tensors have no version and are written as before
+    with torch.inference_mode():
+        t = torch.zeros(300, device="cuda")
+        prism.adamw_step([t], [torch.ones(300, device="cuda")], lr=0.5, **prism.adamw_state([t]))
+    assert torch.allclose(t, torch.full_like(t, -0.5))
