@@ -466,6 +466,11 @@ int prism_embed_bwd(const void* ids, const void* d_out, const int32_t* lengths, 
                     float scale, int ids_bits, int dtype, int accumulate, float* d_table,
                     void* workspace, size_t workspace_bytes, prism_stream_t stream);
 
+/* Test hook, process-wide: with `on` not 0 the sort of prism_embed_bwd takes no cluster of more than
+ * eight blocks, as where the device has no place for one (more than 8192 tokens are then sorted
+ * by tiles).  The results are the same bit for bit. */
+void prism_set_portable_clusters(int on);
+
 /* One parameter tensor of prism_adamw_step: n elements at each of the device pointers. */
 typedef struct prism_adamw_tensor {
   void* param;            /* p_dtype, updated in place */

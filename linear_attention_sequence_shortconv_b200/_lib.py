@@ -62,6 +62,7 @@ EXPORTS = (
     "prism_scan_fwd_split_chunks",
     "prism_stream_status",
     "prism_set_spin_limit",
+    "prism_set_portable_clusters",
     "prism_set_split_event",
     "prism_status_string",
     "prism_version",
@@ -148,6 +149,8 @@ def lib() -> ctypes.CDLL:
     L.prism_stream_status.restype = ci
     L.prism_set_spin_limit.argtypes = [ctypes.c_longlong]
     L.prism_set_spin_limit.restype = None
+    L.prism_set_portable_clusters.argtypes = [ci]
+    L.prism_set_portable_clusters.restype = None
     L.prism_set_split_event.argtypes = [vp]
     L.prism_set_split_event.restype = None
     L.prism_status_string.argtypes = [ci]
@@ -534,3 +537,9 @@ def stream_status(stream=None) -> int:
 
 def set_spin_limit(limit: int) -> None:
     lib().prism_set_spin_limit(int(limit))
+
+
+def set_portable_clusters(on: bool) -> None:
+    """Test hook: the embedding gradient takes no cluster of more than eight blocks, as where the
+    device has no place for one."""
+    lib().prism_set_portable_clusters(int(on))

@@ -27,6 +27,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "embed.cuh"
 #include "rowops.cuh"
@@ -34,6 +35,8 @@
 namespace prism {
 
 namespace {
+
+std::atomic<bool> g_portable_clusters{false};  // prism_set_portable_clusters()
 
 constexpr int kFwdThreads = 256;
 
@@ -806,12 +809,16 @@ cudaError_t embed_fwd_ids(const EmbedParams& p, int table_dtype, int dtype, cuda
   return embed_fwd_types<I, float, float>(p, stream);
 }
 
+// The one-launch sort.  *placed: whether the device has room for its cluster at all, which is certain up
+// to the portable size; a device that is cut into parts may not place a larger one.
 template <typename I, int KPT>
-cudaError_t sort_cluster(const EmbedParams& p, const EmbedPlan& plan, cudaStream_t stream) {
+cudaError_t sort_cluster(const EmbedParams& p, const EmbedPlan& plan, cudaStream_t stream, bool* placed) {
+  *placed = plan.cluster <= kPortableCluster || !g_portable_clusters.load(std::memory_order_relaxed);
+  if (!*placed) return cudaSuccess;
   auto bytes = [](int digit) { return (size_t)kClusterThreads * KPT * 8 + (((size_t)kClusterWarps * 2 + 12) << digit); };
   cudaError_t err = cudaFuncSetAttribute(sort_cluster_kernel<I, KPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)bytes(kEmbedMaxDigit));
-  if (err == cudaSuccess && plan.cluster > 8)
+  if (err == cudaSuccess && plan.cluster > kPortableCluster)
     err = cudaFuncSetAttribute(sort_cluster_kernel<I, KPT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
@@ -825,6 +832,15 @@ cudaError_t sort_cluster(const EmbedParams& p, const EmbedPlan& plan, cudaStream
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  if (plan.cluster > kPortableCluster) {
+    int clusters = 0;
+    err = cudaOccupancyMaxActiveClusters(&clusters, sort_cluster_kernel<I, KPT>, &cfg);
+    if (err != cudaSuccess || clusters < 1) {
+      cudaGetLastError();
+      *placed = false;
+      return cudaSuccess;
+    }
+  }
   return cudaLaunchKernelEx(&cfg, sort_cluster_kernel<I, KPT>, p, plan);
 }
 
@@ -845,8 +861,14 @@ cudaError_t sort_tiles(const EmbedParams& p, const EmbedPlan& plan, cudaStream_t
 }
 
 template <typename I>
-cudaError_t embed_sort(const EmbedParams& p, const EmbedPlan& plan, cudaStream_t stream) {
-  if (plan.cluster) return plan.kpt == 1 ? sort_cluster<I, 1>(p, plan, stream) : sort_cluster<I, 2>(p, plan, stream);
+cudaError_t embed_sort(const EmbedParams& p, EmbedPlan plan, cudaStream_t stream) {
+  if (plan.cluster) {
+    bool placed;
+    const cudaError_t err =
+        plan.kpt == 1 ? sort_cluster<I, 1>(p, plan, stream, &placed) : sort_cluster<I, 2>(p, plan, stream, &placed);
+    if (placed) return err;
+    plan.by_tiles();
+  }
   return plan.kpt == 2 ? sort_tiles<I, 2>(p, plan, stream)
          : plan.kpt == 4 ? sort_tiles<I, 4>(p, plan, stream) : sort_tiles<I, 8>(p, plan, stream);
 }
@@ -879,6 +901,8 @@ cudaError_t embed_sums(const EmbedParams& p, const EmbedPlan& plan, cudaStream_t
 }
 
 }  // namespace
+
+void set_portable_clusters(bool on) { g_portable_clusters.store(on, std::memory_order_relaxed); }
 
 cudaError_t launch_embed_fwd(const EmbedParams& p, int ids_bits, int table_dtype, int dtype, cudaStream_t stream) {
   return ids_bits == 32 ? embed_fwd_ids<int32_t>(p, table_dtype, dtype, stream)

@@ -18,6 +18,7 @@ cudaError_t launch_gated_norm_bwd(const GatedNormParams& p, int d, int gate, int
 cudaError_t launch_block_norm(const BlockNormParams& p, bool bwd, int x_dtype, int dtype, cudaStream_t stream);
 cudaError_t launch_embed_fwd(const EmbedParams& p, int ids_bits, int table_dtype, int dtype, cudaStream_t stream);
 cudaError_t launch_embed_bwd(const EmbedParams& p, int ids_bits, int dtype, cudaStream_t stream);
+void set_portable_clusters(bool on);
 cudaError_t launch_adamw(const AdamTensor* tensors, int count, unsigned blocks, const AdamParams& a, int p_dtype,
                          int g_dtype, int bits, cudaStream_t stream);
 }  // namespace prism
@@ -274,6 +275,8 @@ int prism_embed_bwd(const void* ids, const void* d_out, const int32_t* lengths, 
   p.scale = scale;
   return launched(prism::launch_embed_bwd(p, ids_bits, dtype, cuda_stream(stream)));
 }
+
+void prism_set_portable_clusters(int on) { prism::set_portable_clusters(on != 0); }
 
 int prism_adamw_step(const prism_adamw_tensor* tensors, int count, int step, const int32_t* step_dev, double lr,
                      const float* lr_dev, double beta1, double beta2, double eps, const float* grad_scale, int p_dtype,

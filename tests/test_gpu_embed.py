@@ -245,3 +245,22 @@ def test_subnormal_numbers_are_added_to_and_kept(D, kind):
     assert torch.equal(got.double().cpu(), want)
     dense = prism.embed_bwd(ids.cuda(), d.cuda(), V)
     assert torch.equal(dense.double().cpu(), want - old.double())
+
+
+@pytest.mark.parametrize("N,V,D,bits", [(8193, 1023, 24, 32), (16384, 1024, 40, 64), (16385, 70000, 8, 32),
+                                        (30001, 1 << 20, 16, 64), (32768, 32000, 64, 32)])
+def test_without_a_large_cluster_the_gradient_is_the_same(N, V, D, bits):
+    # more tokens than eight blocks sort: by tiles where the device has no place for sixteen
+    ids, d = _ids(1, N, V, bits, "zipf").cuda(), torch.randn((1, N, D), generator=_gen(2)).cuda()
+    lens = torch.tensor([N - 3], dtype=torch.int32).cuda()
+    old = torch.randn((V, D), generator=_gen(3))
+    runs = []
+    try:
+        for portable in (False, True):
+            prism.set_portable_clusters(portable)
+            added = prism.embed_bwd(ids, d, V, lengths=lens, d_table=old.cuda(), accumulate=True)
+            runs.append([prism.embed_bwd(ids, d, V), prism.embed_bwd(ids, d, V, lengths=lens), added])
+    finally:
+        prism.set_portable_clusters(False)
+    assert prism.stream_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
