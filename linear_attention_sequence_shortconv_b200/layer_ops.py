@@ -363,6 +363,8 @@ def _list_checks(tensors, name, dtype, params, dev, shapes=True):
         raise ValueError(f"{name} must have {len(params)} tensors, got {len(tensors)}")
     at = dev.index
     for t, p in zip(tensors, params):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must hold tensors, got {type(t).__name__}")
         if t.dtype == dtype and t.get_device() == at and t.is_contiguous() and (not shapes or t.shape == p.shape):
             continue
         if t.dtype != dtype:
@@ -432,9 +434,12 @@ def _adamw_table(n, lists, decay, dev):
                                  for x in (*(_DL_TYPES[dtype] if tensors is not None else (0, 0)),
                                            STATE_BLOCK if blocks else 0)])
         objects = array.array("Q", map(id, itertools.chain.from_iterable(given)))
-        if gather(len(lists), spec.buffer_info()[0], n, objects.buffer_info()[0], view, dev.index,
-                  ctypes.create_string_buffer(_DL_TENSOR * n), table, _ADAMW_TENSOR, 56) < 0:
-            return table
+        try:
+            if gather(len(lists), spec.buffer_info()[0], n, objects.buffer_info()[0], view, dev.index,
+                      ctypes.create_string_buffer(_DL_TENSOR * n), table, _ADAMW_TENSOR, 56) < 0:
+                return table
+        except Exception:  # torch's function says so of an object that is no tensor
+            pass
         # the checks below say what is wrong with which
     fields = memoryview(table).cast("B").cast("Q")
     params = lists[0][1]

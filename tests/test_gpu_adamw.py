@@ -354,3 +354,20 @@ def test_infinite_parameters_stay(bits, wd):
     want = torch.full((700,), 0.5 * (1 - 0.1 * wd))
     want[3], want[300], want[699] = -inf, inf, -inf
     assert torch.allclose(p[0].cpu(), want, rtol=2 * U, atol=0)
+
+
+@pytest.mark.parametrize("slow", [False, True])
+def test_what_is_no_tensor_is_named(slow, monkeypatch):
+    # such as the gradient of a parameter that took no part
+    if slow:
+        monkeypatch.setattr(layer_ops, "_dl_exchange", lambda: None)
+    p = [torch.ones(300, device="cuda") for _ in range(3)]
+    g = [torch.ones(300, device="cuda"), None, torch.ones(300, device="cuda")]
+    state = prism.adamw_state(p)
+    with pytest.raises(TypeError, match="grads.*NoneType"):
+        prism.adamw_step(p, g, **state)
+    with pytest.raises(TypeError, match="params.*float"):
+        prism.adamw_step([p[0], 1.0, p[2]], [g[0], g[2], g[0]], **state)
+    with pytest.raises(TypeError, match="exp_avg_sq.*list"):
+        prism.adamw_step(p[:2], g[::2], state["exp_avg"][:2], [state["exp_avg_sq"][0], [1.0]])
+    assert all(t.eq(1).all() for t in p)
