@@ -7,6 +7,7 @@ fp32 of n terms, in any grouping: at most n roundings, and three for the factor,
 and the addition to what was there, each relative to the sum of the magnitudes.
 """
 import math
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -264,3 +265,70 @@ def test_without_a_large_cluster_the_gradient_is_the_same(N, V, D, bits):
         prism.set_portable_clusters(False)
     assert prism.stream_status() == 0
     assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+@pytest.mark.parametrize("N", [16384, 16385, 32768, 32769])
+@pytest.mark.parametrize("V,bits", [(900, 32), (30000, 64), (1 << 20, 32)])  # one, two and three passes
+def test_gradient_where_the_sort_changes_its_form(N, V, bits):
+    # small integers, so that every sum is exact: the last batch with one pair a thread, the last one that
+    # a cluster sorts (full), and their successors
+    D = 24
+    ids = _ids(1, N, V, bits, "zipf").cuda()
+    d = torch.randint(-8, 9, (1, N, D), generator=_gen(4)).float().cuda()
+    want = torch.zeros((V, D), dtype=torch.float64, device="cuda").index_add_(0, ids.view(-1).long(), d.view(N, D).double())
+    assert torch.equal(prism.embed_bwd(ids, d, V).double(), want)
+    old = torch.randint(-99, 99, (V, D), generator=_gen(5)).float().cuda()
+    got = prism.embed_bwd(ids, d, V, d_table=old.clone(), accumulate=True)
+    assert torch.equal(got.double(), want + old) and prism.stream_status() == 0
+
+
+@pytest.mark.parametrize("V,D,dtype", [(2, 264, "bf16"), (3000, 257, "fp32"), (40, 520, "bf16")])
+def test_gradient_of_very_many_tokens_over_several_column_tiles(V, D, dtype):
+    # more than 16384 chunks of partial sums, folded and joined for each tile of 256 columns; exact as above
+    N = 2_200_003
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    ids = (torch.rand((1, N), generator=gen, device="cuda") ** 2 * V).int().clamp_(max=V - 1)
+    d = torch.randint(0, 4, (1, N, D), generator=gen, device="cuda").to(DT[dtype])
+    lens = torch.tensor([N - 7], dtype=torch.int32, device="cuda")
+    got = prism.embed_bwd(ids, d, V, lengths=lens)
+    want = torch.zeros((V, D), device="cuda")
+    for a in range(0, N - 7, 100_000):  # sums below 2^24: exact in any order
+        b = min(a + 100_000, N - 7)
+        want.index_add_(0, ids[0, a:b], d[0, a:b].float())
+    assert want.max() < 2 ** 24 and torch.equal(got, want) and prism.stream_status() == 0
+    assert torch.equal(prism.embed_bwd(ids, d, V, lengths=lens), got)
+
+
+@pytest.mark.parametrize("N,V,D", [(20000, 50000, 40), (70000, 3000, 64), (200000, 1 << 20, 8), (300001, 2, 16),
+                                   (300000, 900, 9)])
+def test_every_form_of_the_gradient_repeats_bit_for_bit(N, V, D):
+    # the cluster, the tiles, the fold and the join of many chunks: twice, from another stream, from a
+    # captured graph and from two threads at once
+    ids = _ids(1, N, V, 64, "zipf").cuda()
+    d = torch.randn((1, N, D), generator=_gen(7)).cuda()
+    first = prism.embed_bwd(ids, d, V, scale=1.7)
+    again = prism.embed_bwd(ids, d, V, scale=1.7)
+    assert torch.equal(first, again)
+    torch.cuda.synchronize()
+
+    def other(_):
+        s = torch.cuda.Stream()
+        out = [prism.embed_bwd(ids, d, V, scale=1.7, stream=s) for _ in range(4)]
+        s.synchronize()
+        return out
+
+    with ThreadPoolExecutor(2) as pool:
+        for outs in pool.map(other, range(2)):
+            assert all(torch.equal(t, first) for t in outs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = prism.embed_bwd(ids, d, V, scale=1.7)
+    for _ in range(2):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    ids.copy_(_ids(1, N, V, 64, "even", 3))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, prism.embed_bwd(ids, d, V, scale=1.7)) and prism.stream_status() == 0

@@ -7,6 +7,7 @@ for gradients, relative to the largest value (the operators around the mixer add
 of 2^-24, far below).
 """
 import math
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -266,3 +267,41 @@ def test_autograd_sees_what_a_call_writes():
         t = torch.zeros(300, device="cuda")
         prism.adamw_step([t], [torch.ones(300, device="cuda")], lr=0.5, **prism.adamw_state([t]))
     assert torch.allclose(t, torch.full_like(t, -0.5))
+
+
+def test_two_threads_call_at_once():
+    # the gated norm, the lookup and the AdamW step from two host threads, each on a stream of its own
+    def inputs(k):
+        g = torch.Generator().manual_seed(k)
+        r = lambda *s: torch.randn(s, generator=g).cuda()  # noqa: E731
+        ids = torch.randint(0, 500, (2, 300), generator=g).cuda()
+        return dict(o=r(2, 300, 3, 64 << k), gate=r(2, 300, 3, 64 << k), w=r(64 << k), dy=r(2, 300, 3, 64 << k), ids=ids,
+                    table=r(500, 40 + k), p=[r(700 + k), r(3, 5000)], g=[r(700 + k), r(3, 5000)])
+
+    def run(x, s):
+        p = [t.clone() for t in x["p"]]
+        state = prism.adamw_state(p, bits=8)
+        if s is not None:
+            s.wait_stream(torch.cuda.current_stream())
+        out = [prism.gated_norm_fwd(x["o"], x["gate"], x["w"], stream=s),
+               *prism.gated_norm_bwd(x["o"], x["gate"], x["w"], x["dy"], stream=s).values(),
+               prism.embed_fwd(x["ids"], x["table"], stream=s)]
+        for step in (1, 2):
+            prism.adamw_step(p, x["g"], step=step, stream=s, **state)
+        return out + p + [t.float() if s is None else t for n in state for t in state[n]]
+
+    work = [inputs(k) for k in (0, 1)]
+    want = [run(x, None) for x in work]
+    torch.cuda.synchronize()
+
+    def many(x):
+        s = torch.cuda.Stream()
+        out = [run(x, s) for _ in range(20)]
+        s.synchronize()
+        return out
+
+    with ThreadPoolExecutor(2) as pool:
+        for outs, first in zip(pool.map(many, work), want):
+            for out in outs:
+                assert all(torch.equal(a.float(), b) for a, b in zip(out, first))
+    assert prism.stream_status() == 0
