@@ -332,3 +332,15 @@ def test_every_form_of_the_gradient_repeats_bit_for_bit(N, V, D):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, prism.embed_bwd(ids, d, V, scale=1.7)) and prism.stream_status() == 0
+
+
+@pytest.mark.parametrize("N,V,D", [(3000, 500, 3), (40000, 9000, 8), (300000, 40, 24)])
+def test_sums_of_several_calls_add_up(N, V, D):
+    # rows that share a sector of the table, call after call; integers, so that every sum is exact
+    ids = _ids(1, N, V, 32, "zipf").cuda()
+    table, want = torch.zeros((V, D), device="cuda"), torch.zeros((V, D), dtype=torch.float64, device="cuda")
+    for k in range(4):
+        d = torch.randint(-8, 9, (1, N, D), generator=_gen(k)).float().cuda()
+        prism.embed_bwd(ids, d, V, d_table=table, accumulate=True)
+        want.index_add_(0, ids.view(-1), d.view(N, D).double())
+    assert torch.equal(table.double(), want) and prism.stream_status() == 0
