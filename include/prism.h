@@ -94,7 +94,7 @@ enum prism_status {
   PRISM_OK = 0,
   PRISM_ERR_INVALID_ARG = 1, /* NULL where required, non-positive size, L < 1, W < 1, ... */
   PRISM_ERR_UNSUPPORTED = 2, /* valid but not implemented: head size, width, alignment, device */
-  PRISM_ERR_WORKSPACE = 3,   /* workspace smaller than prism_scan_fwd_workspace_size() */
+  PRISM_ERR_WORKSPACE = 3,   /* workspace smaller than the call's workspace_size query */
   PRISM_ERR_CUDA = 4,        /* a CUDA runtime call or kernel launch failed */
   PRISM_ERR_TIMEOUT = 5,     /* a bounded device-side wait expired (from prism_stream_status) */
   PRISM_ERR_BOUNDS = 6       /* an id outside the table of prism_embed_fwd / prism_embed_bwd, or,
@@ -370,8 +370,8 @@ int prism_decode_step(const void* q, const void* k, const void* v,
  * stream; before the first layer stands the embedding, behind the backward pass the optimiser.
  * They follow the conventions above: dense device buffers, 16-byte aligned, no allocation and
  * no synchronisation, statistics and sums in fp32, each output rounded once.  Rows of padding
- * (t >= lengths[b]) are not read; their outputs are written as zero and they add nothing to
- * the gradients of weights.  Every result is the same bit for bit on every run.  Weights and
+ * (t >= lengths[b]) are not read; their outputs are written as zero, whatever the weights hold, and
+ * they add nothing to the gradients of weights.  Every result is the same bit for bit on every run.  Weights and
  * their gradients are fp32; activations and their gradients have the dtype of the call.  A
  * buffer that a call writes may overlap no other buffer of the call, except where an argument
  * below says that it may be exactly another one (PRISM_ERR_INVALID_ARG otherwise).
@@ -387,6 +387,9 @@ int prism_decode_step(const void* q, const void* k, const void* v,
  *   weight  [d] fp32, shared by the heads
  *   y       [B,T,H,d] dtype (output); may be o
  * d in {16, 32, 64, 128}; eps > 0; act is a prism_act.  One launch.
+ * With PRISM_BF16 the sigmoid is taken from the hardware's approximate exponential and reciprocal, here
+ * and in the backward (d_weight among them): relative error below (2 + 1.2 |gate|) 2^-23 and 2^-22, and
+ * a sigmoid below 2^-126 is zero.  With PRISM_FP32 it is computed with expf and a division.
  */
 int prism_gated_norm_fwd(const void* o, const void* gate, const float* weight, const int32_t* lengths,
                          int B, int T, int H, int d, long long gate_stride, float eps, int act, int dtype,
@@ -415,7 +418,7 @@ int prism_gated_norm_bwd(const void* o, const void* gate, const float* weight, c
  *   y, h      [B,T,D] dtype
  *   weight, post_weight (or NULL), scale (or NULL: 1)  [D] fp32
  * 1 <= D <= PRISM_MAX_WIDTH (any width; multiples of 8, of 4 with an
- * fp32 stream, take wide accesses).  x_dtype and
+ * fp32 stream, take wide accesses); B T <= 2e9 for D > 256.  x_dtype and
  * dtype: both PRISM_BF16, both PRISM_FP32, or an fp32 stream with bf16 blocks.  One launch.
  */
 int prism_block_norm_fwd(const void* x, const void* y, const float* post_weight, const float* scale,
@@ -457,8 +460,9 @@ int prism_embed_fwd(const void* ids, const void* table, const int32_t* lengths, 
  *   the sums are added to what d_table holds and only the rows that a token names are touched
  * Ids outside [0, V) give no gradient and are recorded as in prism_embed_fwd.  workspace: at
  * least prism_embed_bwd_workspace_size() bytes (16 bytes a token for the sorted ids, up to 2 MB
- * of counts, a bit per table row, and 8 D bytes for each chunk of 16 to 128 tokens).  Three or
- * four launches for up to 32768 tokens, else five to eleven.
+ * of counts, a bit per table row, and 8 D bytes for each chunk of 16 to 128 tokens).  Two or three
+ * launches for up to 32768 tokens (up to 8192 where the device has no place for a cluster of sixteen
+ * blocks), else five to thirteen.
  */
 size_t prism_embed_bwd_workspace_size(int B, int T, int V, int D);
 
@@ -497,7 +501,10 @@ typedef struct prism_adamw_tensor {
  *             least 2^-126); the second moment is held as its square root, and one that is not
  *             zero is never held as zero.  The update takes the moments before that rounding.
  *             Zeros are a valid first state.  An infinity or NaN in a gradient makes its block
- *             NaN.
+ *             NaN.  The quotient of the update is taken by the approximate reciprocal (relative error
+ *             2^-23; with 32 bits it is a division).
+ * The decay lr * weight_decay * p and the update are summed before they are subtracted from p, so that a
+ * decay far below 2^-24 is not lost to the rounding of 1 - lr * weight_decay.
  * All parameters share p_dtype and all gradients g_dtype.  The scalars and the scales are
  * 4-byte aligned.  One launch for up to 440 tensors.
  */

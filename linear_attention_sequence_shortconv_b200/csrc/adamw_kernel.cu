@@ -15,8 +15,10 @@
 //
 // Measured over the 145 tensors (110 M elements) of a 12-layer model of width 768, fp32
 // parameters with bf16 copies: fp32 states and gradients 500 us, 6.6 TB/s, the rate of a copy;
-// 8-bit states and bf16 gradients 358 us, 4.9 TB/s (75%): some 50 instructions an element (two
-// roots and conversions both ways among them) share the time with the memory.
+// 8-bit states and bf16 gradients 360 us, 4.9 TB/s (75%): some 50 instructions an element (two
+// roots and conversions both ways among them) share the time with the memory.  In a captured graph, with
+// the step and the rate on the device, whose powers every block computes first: 32 bits 491 us (host
+// scalars 491), 8 bits 363 (353), five small tensors 8.2 (6.2).
 #include "adamw.cuh"
 #include "rowops.cuh"
 

@@ -177,7 +177,9 @@ __device__ __forceinline__ int block_exclusive_scan(int x, int warps, int* warp_
 // pass's pairs before the next one's reads.
 //
 // Against tiles over all SMs: 32768 tokens 14.5 us here and 26 us by tiles; 131072 tokens 41 us
-// (eight pairs a thread, bound by the instructions of 16 SMs) and 26 us.
+// (eight pairs a thread, bound by the instructions of 16 SMs) and 26 us.  Of the whole gradient, whose
+// chained launches overlap: two passes, 8193 tokens 35.1 us here and 41.0 by tiles, 32768 tokens 38.9
+// and 41.8; one pass 33.2 and 32.1, three passes 48.4 and 45.1 at 32768.
 constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
 
 template <typename I, int KPT>
@@ -409,7 +411,10 @@ constexpr int kZeroRows = 64;  // table rows per zeroing block, about
 constexpr int kJoinThreads = 512;
 constexpr int kLongChunks = 8;     // chunks whose long runs one block of the join takes
 constexpr int kFold = 64;          // partial sums that are folded into one where a run holds them all
-constexpr int kFoldFrom = 16384;   // chunks from which that is worth a launch
+// Chunks from which that is worth a launch (rows of 32).  Ids over a large table, with the fold and
+// without: 12288 chunks 82 and 76 us, 20480 chunks 92 and 91, 32768 chunks 107 and 113; over 3000 rows 53
+// and 53, 64 and 75, 74 and 97.  Two rows take all: 8192 chunks 33 and 83, 16384 chunks 37 and 145.
+constexpr int kFoldFrom = 16384;
 constexpr int kShortRun = 8;       // partial sums behind a run's first up to which one thread group joins it
 
 // Eight columns as they lie in memory.
