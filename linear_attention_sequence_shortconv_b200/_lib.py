@@ -183,12 +183,12 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _dtype_code(t: torch.Tensor) -> int:
+def _dtype_code(t: torch.Tensor, name: str = "q/k/v/u/gain") -> int:
     if t.dtype == torch.bfloat16:
         return PRISM_BF16
     if t.dtype == torch.float32:
         return PRISM_FP32
-    raise TypeError(f"q/k/v/u/gain must be bfloat16 or float32, got {t.dtype}")
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
 CHAINS = {"linear": PRISM_CHAIN_LINEAR, "gelu": PRISM_CHAIN_GELU}

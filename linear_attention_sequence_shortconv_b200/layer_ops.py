@@ -137,7 +137,7 @@ def gated_norm_fwd(o, gate, weight, lengths=None, eps: float = 1e-5, act: str = 
     """
     act_code = _act_code(act)
     dev = _call_device(o, stream)
-    code = _dtype_code(o)
+    code = _dtype_code(o, "o")
     sizes = B, T, H, d = _heads(o)
     _check(o, "o", device=dev)
     stride = _gate_stride(gate, o, sizes)
@@ -161,7 +161,7 @@ def gated_norm_bwd(o, gate, weight, dy, lengths=None, eps: float = 1e-5, act: st
     both in o's dtype, and weight (fp32).  "o" is what scan_bwd takes as dO."""
     act_code = _act_code(act)
     dev = _call_device(o, stream)
-    code = _dtype_code(o)
+    code = _dtype_code(o, "o")
     sizes = B, T, H, d = _heads(o)
     _check(o, "o", device=dev)
     stride = _gate_stride(gate, o, sizes)
@@ -219,7 +219,7 @@ def block_norm_fwd(x, weight, y=None, post_weight=None, scale=None, res_scale: f
     dt = y.dtype if y is not None else (h_dtype or x.dtype)
     if h_dtype is not None and h_dtype != dt:
         raise TypeError(f"h has y's dtype {dt}, got h_dtype={h_dtype}")
-    x_code = _dtype_code(x)
+    x_code = _dtype_code(x, "x")
     if dt not in (torch.bfloat16, torch.float32):
         raise TypeError(f"y and h must be bfloat16 or float32, got {dt}")
     code = PRISM_BF16 if dt == torch.bfloat16 else PRISM_FP32
@@ -250,7 +250,7 @@ def block_norm_bwd(x_out, weight, dh, y=None, post_weight=None, scale=None, res_
     weight, post_weight and scale (fp32); None for what was not given.  dx_out None is zero."""
     dev = _call_device(x_out, stream)
     B, T, D = _block_checks(x_out, weight, y, post_weight, scale, lengths, dev)
-    x_code, code = _dtype_code(x_out), _dtype_code(dh)
+    x_code, code = _dtype_code(x_out, "x_out"), _dtype_code(dh, "dh")
     _check(dh, "dh", None if y is None else y.dtype, shape=x_out.shape, device=dev)
     _check(dx_out, "dx_out", x_out.dtype, required=False, shape=x_out.shape, device=dev)
     with _on(dev, stream, (x_out, weight, dh, y, post_weight, scale, dx_out, lengths, workspace)):
@@ -299,7 +299,7 @@ def embed_fwd(ids, table, scale: float = 1.0, lengths=None, dtype: Optional[torc
     if table.dim() != 2:
         raise ValueError(f"table must be [V, D], got {tuple(table.shape)}")
     V, D = _table_sizes(*table.shape)
-    table_code = _dtype_code(table)
+    table_code = _dtype_code(table, "table")
     dt = dtype or (table.dtype if out is None else out.dtype)
     if dt not in (torch.bfloat16, torch.float32):
         raise TypeError(f"dtype must be bfloat16 or float32, got {dt}")
@@ -326,7 +326,7 @@ def embed_bwd(ids, d_out, V: int, scale: float = 1.0, lengths=None, d_table=None
     B, T, bits = _id_sizes(ids, lengths)
     _check(ids, "ids", device=dev)
     V, D = _table_sizes(V, d_out.shape[-1])
-    code = _dtype_code(d_out)
+    code = _dtype_code(d_out, "d_out")
     _check(d_out, "d_out", shape=tuple(ids.shape) + (D,), device=dev)
     _check(lengths, "lengths", torch.int32, required=False, shape=(B,), device=dev)
     _check(d_table, "d_table", torch.float32, required=accumulate, shape=(V, D), device=dev)
@@ -477,10 +477,10 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     if n == 0:
         return
     dev = _call_device(params[0], stream)
-    p_code = _dtype_code(params[0])
+    p_code = _dtype_code(params[0], "params")
     if len(grads) != n:
         raise ValueError(f"grads must have {n} tensors, got {len(grads)}")
-    g_code = _dtype_code(grads[0])
+    g_code = _dtype_code(grads[0], "grads")
     state_dtype = exp_avg[0].dtype if len(exp_avg) else None
     if state_dtype not in (torch.float32, torch.float8_e4m3fn):
         raise TypeError(f"exp_avg must be float32 or float8_e4m3fn, got {state_dtype}")

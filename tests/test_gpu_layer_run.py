@@ -305,3 +305,21 @@ def test_two_threads_call_at_once():
             for out in outs:
                 assert all(torch.equal(a.float(), b) for a, b in zip(out, first))
     assert prism.stream_status() == 0
+
+
+def test_a_refused_type_names_its_argument():
+    o, x, w = torch.zeros(2, 3, H, d, device="cuda"), torch.zeros(2, 3, D, device="cuda"), torch.ones(D, device="cuda")
+    ids, table = torch.zeros((2, 3), dtype=torch.int64, device="cuda"), torch.zeros(V, D, device="cuda")
+    p = [torch.zeros(300, device="cuda")]
+    half = torch.float16
+    for name, call in (("^o ", lambda: prism.gated_norm_fwd(o.to(half), None, w[:d])),
+                       ("^o ", lambda: prism.gated_norm_bwd(o.to(half), None, w[:d], o)),
+                       ("^x ", lambda: prism.block_norm_fwd(x.to(half), w)),
+                       ("^x_out ", lambda: prism.block_norm_bwd(x.to(half), w, x)),
+                       ("^dh ", lambda: prism.block_norm_bwd(x, w, x.to(half))),
+                       ("^table ", lambda: prism.embed_fwd(ids, table.to(half))),
+                       ("^d_out ", lambda: prism.embed_bwd(ids, x.to(half), V)),
+                       ("^params ", lambda: prism.adamw_step([p[0].to(half)], p, p, p)),
+                       ("^grads ", lambda: prism.adamw_step(p, [p[0].to(half)], p, p))):
+        with pytest.raises(TypeError, match=name + ".*float16"):
+            call()
