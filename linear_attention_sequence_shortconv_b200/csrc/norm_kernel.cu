@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kGnThreads) gated_norm_fwd_kernel(GatedNormPar
         y[i] = mul2(y[i], GATE == kGateSilu ? mul2(g, sg) : sg);
       }
     }
-    if (!r[u].valid) zero_pairs(y);  // a weight need not be finite
+    // a weight need not be finite (asked of the call first: without that fp32 rows of 128 take 49 us, not 47)
+    if (p.lengths && !r[u].valid) zero_pairs(y);
     store_shared8<kWide>(static_cast<T*>(p.y) + r[u].row * d, lane, LPR, d, y);
   }
 }
