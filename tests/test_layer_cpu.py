@@ -293,3 +293,12 @@ def test_sizes_beyond_32_bits_are_refused():
     assert layer_ops._stream_rows(meta((1 << 31) - 1, 1)) == ((1 << 31) - 1, 1, 1)
     assert layer_ops._id_sizes(meta(2, 3, dtype=torch.int32), None) == (2, 3, 32)
     assert layer_ops._table_sizes(100, 8) == (100, 8) and layer_ops._step_number(7) == 7
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_block_norm_refuses_more_wide_rows_than_32_bits_number(bwd):
+    far = {n: 0x1000_0000_0000 * (i + 1) for i, n in enumerate(("x", "y", "post", "scale", "weight", "x_out", "h", "dh",
+                                                                "dx_out", "dw", "dpost", "dscale", "ws"))}
+    assert _block(bwd, B=1 << 16, T=1 << 15, D=257, **far) == UNSUPPORTED
+    assert prism.lib().prism_block_norm_bwd_workspace_size(1 << 16, 1 << 15, 257) == 0
+    assert prism.lib().prism_block_norm_bwd_workspace_size(1 << 16, 1 << 15, 256) > 0
